@@ -361,6 +361,176 @@ int qwen2_quantize_q8_0(const uint16_t *w, int64_t rows, int64_t k, int8_t *q, u
  * k. */
 int qwen2_quantize_q4_0(const uint16_t *w, int64_t rows, int64_t k, uint8_t *packed, uint16_t *d);
 
+/* ======================================================================
+ * Paged key / value cache
+ *
+ * A cache held as a pool of pages of page_size positions each, in 16 or 8
+ * bits, and the operators around it: the write of projected rows (per-head
+ * norms, position rotation and quantisation in one pass), the read back
+ * into contiguous rows, and the attention of new rows over the pages --
+ * single tokens, chunks, whole prompts, or another sequence's states.
+ * They need no context: every buffer is the caller's, nothing is allocated,
+ * and the calls are asynchronous on `stream` (a cudaStream_t; NULL = legacy
+ * default stream) of the current device, which must be the device of every
+ * pointer.  All of them may be captured into a CUDA graph: lengths, starts
+ * and page tables are device memory that a replay reads anew.  Errors are
+ * return codes (nothing launched); qwen2_last_error(NULL) has the message.
+ * Values in device memory cannot be checked on the host: see `guard`.
+ * ====================================================================== */
+
+#define QWEN2_DTYPE_F32   0
+#define QWEN2_DTYPE_F16   1
+#define QWEN2_DTYPE_BF16  2
+
+#define QWEN2_KV_F16      0   /* IEEE binary16 */
+#define QWEN2_KV_BF16     1   /* bfloat16 */
+#define QWEN2_KV_INT8     2   /* int8 codes in [-127, 127], one f32 scale per (position, kv head):
+                                 scale = max|x| / 127 (1 where max|x| = 0),
+                                 code = round-half-away(x / scale); value = scale * code */
+#define QWEN2_KV_E4M3     3   /* 8-bit floats (4 exponent, 3 mantissa bits), one f32 scale per
+                                 (position, kv head): scale = max|x| / 448 (1 where max|x| = 0),
+                                 code = e4m3(x / scale), nearest even */
+
+/* Guard codes the paged operators write (first one wins). */
+#define QWEN2_GUARD_POSITION 1  /* a position outside the sequence's pages, the rotation table, or below 0 */
+#define QWEN2_GUARD_SHAPE    3  /* q_start not ascending or past n_rows, more than max_q rows in a sequence */
+#define QWEN2_GUARD_TIMEOUT  4  /* a kernel's bounded wait gave up (outputs are not complete) */
+#define QWEN2_GUARD_PAGE     5  /* a page id outside [0, n_pages) */
+
+/* Rows of heads in device memory: element i of head h of row r is
+ * data[r * row_stride + h * head_stride + i], strides in elements.  data
+ * 16-byte aligned, both strides multiples of 16 bytes (>= 0). */
+typedef struct qwen2_rows {
+    void *data;
+    int32_t dtype;          /* QWEN2_DTYPE_* */
+    int64_t row_stride;
+    int64_t head_stride;
+} qwen2_rows;
+
+/* A pool of pages.  Element i of kv head h at offset t of page p is
+ * k[p * page_stride + t * token_stride + h * head_stride + i] (v alike),
+ * strides in elements; both token-major and head-major pages, and K and V
+ * interleaved in one pool, are strides.  k and v 16-byte aligned, strides
+ * multiples of 16 bytes.  k_scale, v_scale (8-bit formats; else ignored):
+ * f32 [n_pages][n_kv_head][page_size], contiguous, 16-byte aligned. */
+typedef struct qwen2_paged_kv {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int32_t format;         /* QWEN2_KV_* */
+    int32_t n_pages;
+    int32_t page_size;      /* 16, 32, 64, 128 or 256 */
+    int32_t n_kv_head;
+    int32_t head_dim;       /* 64 or 128 */
+    int64_t page_stride, token_stride, head_stride;
+} qwen2_paged_kv;
+
+/* The new rows of a batch of sequences and their pages, all arrays in
+ * device memory.  Sequence s owns rows q_start[s] .. q_start[s+1] - 1 (none
+ * is allowed); with n of them, row i of the sequence stands at position
+ * kv_len[s] - n + i, and position p of the sequence lives at offset
+ * p % page_size of page pages[s * pages_stride + p / page_size].
+ *   n_rows  rows the row buffers hold; rows from q_start[n_seq] on are
+ *           neither read nor written (a padded batch)
+ *   max_q   an upper bound on the rows of any one sequence
+ *   guard   nullable device int32, zeroed by the caller: the first guard
+ *           code that trips is stored there.  A row whose position or page
+ *           is bad is not written; keys in a bad page are left out of the
+ *           attention.  Bad values never lead to an access outside the
+ *           buffers described here. */
+typedef struct qwen2_paged_batch {
+    int32_t n_seq;          /* 1 .. 4096 */
+    int32_t n_rows;
+    int32_t max_q;
+    int32_t max_pages;      /* entries of one sequence's page table row */
+    int64_t pages_stride;
+    const int32_t *q_start; /* [n_seq + 1], ascending from 0 */
+    const int32_t *kv_len;  /* [n_seq], the new rows included */
+    const int32_t *pages;   /* [n_seq][pages_stride] */
+    int32_t *guard;
+} qwen2_paged_batch;
+
+/* What the write does to the rows on their way. */
+typedef struct qwen2_paged_write_opts {
+    const float *q_norm, *k_norm; /* nullable device f32 [head_dim]: RMSNorm of every query / key head,
+                                     x / sqrt(mean(x^2) + norm_eps) * weight */
+    float norm_eps;
+    const float *rope;      /* nullable device f32 [rope_rows][rotary_dim / 2][2], (cos, sin) of each
+                               position (qwen2_rope_table), 16-byte aligned */
+    int32_t rope_rows;
+    int32_t rotary_dim;     /* leading dims of each head that turn: a multiple of 16, at most head_dim */
+    int32_t interleaved;    /* 0: dim i pairs with i + rotary_dim / 2 (NeoX); 1: 2i with 2i + 1 */
+} qwen2_paged_write_opts;
+
+/* Rotation tables for long contexts. */
+#define QWEN2_ROPE_PLAIN  0   /* theta_i = theta^(-2i / rotary_dim) */
+#define QWEN2_ROPE_LINEAR 1   /* position interpolation: every angle divided by factor */
+#define QWEN2_ROPE_YARN   2   /* YaRN (NTK-by-parts): dims that turn more than beta_fast times within
+                                 original_rows keep theta_i, those that turn less than beta_slow times
+                                 divide it by factor, a linear ramp over the dims between; cos and sin
+                                 are multiplied by 0.1 ln(factor) + 1 */
+typedef struct qwen2_rope_scaling {
+    int32_t kind;           /* QWEN2_ROPE_* */
+    double factor;          /* >= 1 */
+    int32_t original_rows;  /* YARN: the context length the model was trained at */
+    double beta_fast, beta_slow;  /* YARN: 32 and 1 in the publication */
+} qwen2_rope_scaling;
+
+/* Host only: fill table, f32 [rows][rotary_dim / 2][2], with (cos, sin) of
+ * position * theta_i, computed in double.  scaling NULL: plain. */
+int qwen2_rope_table(int32_t rows, int32_t rotary_dim, double theta, const qwen2_rope_scaling *scaling,
+                     float *table);
+
+/* Store the k and v rows of a batch in its pages at their positions, k (and
+ * q, if given) normed and rotated on the way, and write the finished queries
+ * to q_out.  The arithmetic is f32; q_out, and f16 / bf16 pages, are rounded
+ * once (nearest even), 8-bit pages as their format says.
+ *   q, q_out  both or neither; n_head heads; q_out f16 or bf16 and not
+ *             overlapping any input
+ *   k, v      n_kv_head heads, the same dtype as q
+ *   opts      nullable
+ * Every position a call writes must belong to one row of the call: two rows
+ * that name one (page, offset) race.  Pages may be shared by sequences that
+ * only read them.  Rows with a negative position (kv_len below the row
+ * count) are not written. */
+int qwen2_paged_write(const qwen2_paged_kv *kv, const qwen2_paged_batch *batch, const qwen2_paged_write_opts *opts,
+                      int32_t n_head, const qwen2_rows *q, const qwen2_rows *q_out, const qwen2_rows *k,
+                      const qwen2_rows *v, void *stream);
+
+/* Read pages back: position p of sequence s goes to row out_start[s] + p of
+ * k and v (f32, f16 or bf16, one dtype), for p < min(kv_len[s],
+ * out_start[s + 1] - out_start[s]).  out_start: device int32 [n_seq + 1],
+ * ascending; rows outside are left as they were, and so are rows whose
+ * page is bad.  n_out: rows the outputs hold.  batch->q_start, n_rows and
+ * max_q are not used.  8-bit values are scale * code in f32, then rounded
+ * once to a 16-bit dtype. */
+int qwen2_paged_read(const qwen2_paged_kv *kv, const qwen2_paged_batch *batch, const int32_t *out_start,
+                     int32_t n_out, const qwen2_rows *k, const qwen2_rows *v, void *stream);
+
+/* Attention of the batch's rows over its pages:
+ *   o = sum_j softmax_j(scale * q . k_j) v_j
+ * over the sequence's positions j <= the row's own (causal != 0), or all
+ * j < kv_len (causal = 0: another sequence's states).  Query head h reads
+ * kv head h / (n_head / n_kv_head).  Scores, softmax statistics and sums
+ * are f32; the probabilities enter the value product rounded to 16 bits.
+ * A row without a key gives o = 0 and lse = -inf.  What stands in the pages
+ * at positions >= kv_len may be anything, NaN and infinities included; a
+ * non-finite value among a sequence's own kv_len positions may make any of
+ * its rows NaN.
+ *   q       f16 or bf16; the type of the pages where they are 16-bit
+ *   out     q's dtype; may not overlap q
+ *   lse     nullable f32 [n_rows][n_head]: log of the sum of exp(scale q.k)
+ *   workspace  device memory, 256-byte aligned, of
+ *           qwen2_paged_attention_workspace bytes; its contents need not be
+ *           kept between calls.  Calls that may run at the same time (other
+ *           streams, graphs replayed side by side) need a workspace each. */
+int qwen2_paged_attention(const qwen2_paged_kv *kv, const qwen2_paged_batch *batch, int32_t n_head,
+                          const qwen2_rows *q, const qwen2_rows *out, float *lse, float scale, int32_t causal,
+                          void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace bytes of qwen2_paged_attention for these shapes on the current
+ * device; -1 on bad arguments (qwen2_last_error(NULL)). */
+int64_t qwen2_paged_attention_workspace(const qwen2_paged_kv *kv, const qwen2_paged_batch *batch, int32_t n_head);
+
 #ifdef __cplusplus
 }
 #endif

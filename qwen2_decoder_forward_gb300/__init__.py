@@ -58,6 +58,8 @@ EXPORTS = (
     "qwen2_kv_bytes_per_seq", "qwen2_quantize_q8_0", "qwen2_quantize_q4_0", "qwen2_features", "qwen2_profile_marks",
     "qwen2_lm_head_argmax_noalloc", "qwen2_test_raise_guard", "qwen2_test_stall_decode",
     "qwen2_check_canaries",
+    "qwen2_rope_table", "qwen2_paged_write", "qwen2_paged_read", "qwen2_paged_attention",
+    "qwen2_paged_attention_workspace",
 )
 
 
@@ -402,6 +404,41 @@ class Qwen2Model:
         self._check(lib().qwen2_kv_cache(self._h, ctypes.byref(base), dims))
         return torch.as_tensor(_CudaArray(base.value, list(dims), "<f4"), device="cuda")
 
+    def save_pages(self, seq_id: int, n: int, pools, pages, stream=None):
+        """Copy positions 0..n-1 of one sequence's cache into paged pools
+        (``pools``: one PagedKV per layer; ``pages``: int32 CUDA tensor, the
+        page ids of the sequence in every pool), in the pools' format.  The
+        call is ordered on the stream like any other."""
+        self._page_rows(seq_id, n, pools, pages, stream, save=True)
+
+    def load_pages(self, seq_id: int, n: int, pools, pages, stream=None):
+        """Bring positions 0..n-1 that save_pages stored back into a sequence
+        slot of the cache (any slot, any model of the same shape)."""
+        self._page_rows(seq_id, n, pools, pages, stream, save=False)
+
+    def _page_rows(self, seq_id, n, pools, pages, stream, save):
+        import torch
+        s = self.shape
+        if not 0 <= seq_id < self.max_seqs:
+            raise Qwen2Error(QWEN2_E_ARG, f"sequence id {seq_id} outside [0, max_seqs)")
+        if len(pools) != s.n_layer:
+            raise Qwen2Error(QWEN2_E_ARG, f"{len(pools)} pools for {s.n_layer} layers")
+        if not 1 <= n <= self.n_ctx or pages.numel() * pools[0].page_size < n:
+            raise Qwen2Error(QWEN2_E_POS, f"{n} positions need pages for them and n_ctx >= {n}")
+        if any(p.page_size != pools[0].page_size for p in pools):
+            raise Qwen2Error(QWEN2_E_ARG, "the pools of a sequence must have one page size")
+        st = stream if stream is not None else torch.cuda.current_stream()
+        with torch.cuda.stream(st):
+            cache = self.kv_cache()[seq_id]
+            ends = torch.arange(0, 2 * n, n, dtype=torch.int32, device=cache.device)   # [0, n]
+            batch = PagedBatch(ends, ends[1:], pages.view(1, -1), n)
+            for layer, pool in enumerate(pools):
+                k, v = (cache[layer, i, :, :n].transpose(0, 1) for i in (0, 1))
+                if save:
+                    paged_write(pool, batch, k, v)
+                else:
+                    paged_read(pool, batch, ends, n, k_out=k, v_out=v)
+
     def test_raise_guard(self, code: int, stream=None):
         """Test hook: write ``code`` into the device guard word (as a kernel's
         bounded wait does when it gives up); the next synchronize reports it."""
@@ -433,3 +470,7 @@ def _data_ptr(t):
     if not t.is_contiguous():
         raise ValueError("output tensors must be contiguous")
     return ctypes.c_void_p(t.data_ptr())
+
+
+from .paged import (KV_BF16, KV_E4M3, KV_F16, KV_INT8, ROPE_LINEAR, ROPE_PLAIN, ROPE_YARN, PagedBatch,  # noqa: E402
+                    PagedKV, paged_attention, paged_attention_workspace, paged_read, paged_write, rope_table)

@@ -1,0 +1,254 @@
+// Shared by the paged key / value cache operators: the descriptors as the
+// kernels take them, sequence and page lookups with their bounds checks, and
+// the work list of the attention kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/qwen2.h"
+#include "common.cuh"
+
+namespace qwen2 {
+namespace paged {
+
+// The pool and the batch, checked on the host (paged_api.cu).
+struct Pool {
+    char *k, *v;
+    float *k_scale, *v_scale;
+    int n_pages, page_shift;                            // page_size = 1 << page_shift
+    int n_kv;
+    long long page_bytes, token_bytes, head_bytes;      // strides in bytes
+};
+struct Batch {
+    int n_seq, n_rows, max_q, max_pages;
+    long long pages_stride;
+    const int *q_start, *kv_len, *pages;
+    int* guard;
+};
+struct Rows {
+    char* data;
+    long long row_bytes, head_bytes;                    // strides in bytes
+};
+
+// One sequence's rows [q0, q0 + n) and positions [0, kv), clamped to what the
+// buffers hold, so that bad device values never lead outside them.
+struct Seq {
+    int q0, n, kv;
+    bool bad_rows, bad_len;
+};
+__device__ __forceinline__ Seq load_seq(const Batch& b, int page_shift, int s) {
+    Seq r;
+    const int q0 = b.q_start[s], q1 = b.q_start[s + 1], kv = b.kv_len[s];
+    r.bad_rows = q0 < 0 || q1 < q0 || q1 > b.n_rows || q1 - q0 > b.max_q;
+    r.q0 = min(max(q0, 0), b.n_rows);
+    r.n = r.bad_rows ? 0 : q1 - q0;
+    const long long cap = (long long)b.max_pages << page_shift;
+    r.bad_len = kv < 0 || kv > cap;
+    r.kv = r.bad_len ? 0 : kv;
+    return r;
+}
+
+// ---- the attention kernels' work list -------------------------------------------
+// The query rows of one sequence and kv head are the pairs (row, query head of
+// the group), row-major: packed row i = row * group + head.  They are cut into
+// tiles of kRows packed rows, and each tile's keys into units of kKeys
+// positions; a tile without keys is one unit.  The units of all tiles, ordered
+// (sequence, kv head, tile, unit), form one list, of which CTA c of g takes
+// the contiguous part [W c / g, W (c + 1) / g): every CTA has the same work
+// whatever the mix of lengths, and a tile is cut at most where two CTAs'
+// parts meet.  A CTA that covers a whole tile writes its rows itself; the
+// others leave a partial (row maxima, sums, unnormalised rows) that
+// k_attn_join adds up in list order, so results do not depend on timing.
+
+// Keys that the tile of packed rows [i0, i0 + rows) sees: its last row's.
+__device__ __forceinline__ int tile_keys(const Seq& q, int group, int i0, int rows, bool causal) {
+    if (!causal) return q.kv;
+    const int last = (min(i0 + rows, q.n * group) - 1) / group;
+    return max(0, q.kv - q.n + last + 1);
+}
+// Units of one kv head of a sequence, over its tiles.
+__device__ __forceinline__ long long head_units(const Seq& q, int group, int rows, int keys, bool causal) {
+    const int packed = q.n * group;
+    const int tiles = (packed + rows - 1) / rows;
+    if (!causal) return (long long)tiles * max(1, (q.kv + keys - 1) / keys);
+    long long u = 0;
+    for (int t = 0; t < tiles; ++t) u += max(1, (tile_keys(q, group, t * rows, rows, true) + keys - 1) / keys);
+    return u;
+}
+
+// What a CTA left in the workspace: slot 0 the part of a tile that an earlier
+// CTA began, slot 1 the beginning of a tile that goes on in the next CTA.
+struct PartInfo {
+    int q0, packed0, packed_end, head;   // rows of the batch from q0; packed rows [packed0, packed_end) of kv head `head`
+    int state;                           // kPartNone, or bits
+    int pad[3];
+};
+constexpr int kPartNone = 0, kPartUsed = 1, kPartLast = 2;   // kPartLast: the tile ends here
+
+// The workspace of one attention kernel: g CTAs of tiles of `rows` packed rows.
+struct Parts {
+    PartInfo* info;   // [2 g]
+    float* ml;        // [2 g][2][rows]: row maxima (base 2), sums
+    float* o;         // [2 g][rows][hd]
+    int rows;
+};
+__host__ __device__ inline long long parts_bytes(int g, int rows, int hd) {
+    const long long b = 2ll * g * (sizeof(PartInfo) + 2ll * rows * 4 + (long long)rows * hd * 4);
+    return (b + 255) / 256 * 256;
+}
+inline Parts carve_parts(void* ws, int g, int rows) {
+    Parts p;
+    char* c = static_cast<char*>(ws);
+    p.info = reinterpret_cast<PartInfo*>(c);
+    p.ml = reinterpret_cast<float*>(c + 2ll * g * sizeof(PartInfo));
+    p.o = p.ml + 4ll * g * rows;
+    p.rows = rows;
+    return p;
+}
+
+// Everything an attention kernel takes.
+struct AttnArgs {
+    Pool kv;
+    Batch b;
+    Rows q, out;
+    float* lse;              // [n_rows][n_head] or null
+    int n_head, group;
+    int causal;
+    float scale_log2;        // scale * log2(e): the softmax runs in base 2
+    int rows_lo, rows_hi;    // this kernel's sequences: rows_lo < packed rows <= rows_hi
+    Parts parts;
+};
+
+// One CTA's current tile.
+struct Tile {
+    int s, head, t;          // sequence, kv head, tile index
+    Seq q;
+    int keys, units;         // keys the tile sees, and their units
+    int u0, n;               // first unit and number of units of this CTA's part
+};
+
+// Sums of the units of the first s sequences, and the CTA's share; one copy in
+// shared memory per CTA.
+struct WorkList {
+    const long long* prefix;   // shared memory [n_seq + 1]
+    long long begin, end;      // this CTA's units
+};
+
+__device__ __forceinline__ bool owns(const AttnArgs& a, const Seq& q) {
+    const long long packed = (long long)q.n * a.group;
+    return packed > a.rows_lo && packed <= a.rows_hi;
+}
+
+// Builds the prefix sums with the whole block (at most 4096 sequences) and
+// returns this CTA's share.  min_units: a CTA gets at least that many units
+// (but the last), so that small batches are not cut finer than pays.
+template <int kRows, int kKeys>
+__device__ __forceinline__ WorkList build_work(const AttnArgs& a, long long* prefix, int min_units) {
+    for (int s = threadIdx.x; s < a.b.n_seq; s += blockDim.x) {
+        const Seq q = load_seq(a.b, a.kv.page_shift, s);
+        if (blockIdx.x == 0 && (q.bad_rows || q.bad_len))
+            raise_guard(a.b.guard, q.bad_rows ? kGuardShape : kGuardPosition);
+        prefix[s + 1] = owns(a, q) ? head_units(q, a.group, kRows, kKeys, a.causal) * a.kv.n_kv : 0;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        long long carry = 0;
+        for (int s0 = 0; s0 < a.b.n_seq; s0 += 32) {
+            const int s = s0 + threadIdx.x;
+            long long v = s < a.b.n_seq ? prefix[s + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, v, o);
+                if ((int)threadIdx.x >= o) v += u;
+            }
+            v += carry;
+            if (s < a.b.n_seq) prefix[s + 1] = v;
+            carry = __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (threadIdx.x == 0) prefix[0] = 0;
+    }
+    __syncthreads();
+    const long long total = prefix[a.b.n_seq];
+    const long long most = (total + min_units - 1) / min_units;
+    const long long g = most < (long long)gridDim.x ? (most > 0 ? most : 1) : (long long)gridDim.x;
+    WorkList w;
+    w.prefix = prefix;
+    const long long c = blockIdx.x;
+    // total / g and the remainder keep the products within 64 bits.
+    const long long each = total / g, rest = total - each * g;
+    w.begin = c < g ? each * c + (c < rest ? c : rest) : total;
+    w.end = c < g ? w.begin + each + (c < rest ? 1 : 0) : total;
+    return w;
+}
+
+// The tile that holds unit `u` of the list, with up to `left` units of it.
+template <int kRows, int kKeys>
+__device__ __forceinline__ Tile find_tile(const AttnArgs& a, const WorkList& w, long long u, long long left) {
+    int lo = 0, hi = a.b.n_seq;          // largest s with prefix[s] <= u and units of its own
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (w.prefix[mid] <= u) lo = mid;
+        else hi = mid;
+    }
+    Tile t;
+    t.s = lo;
+    t.q = load_seq(a.b, a.kv.page_shift, lo);
+    const long long per_head = (w.prefix[lo + 1] - w.prefix[lo]) / a.kv.n_kv;
+    long long r = u - w.prefix[lo];
+    t.head = (int)(r / per_head);
+    r -= t.head * per_head;
+    if (!a.causal) {
+        t.keys = t.q.kv;
+        t.units = max(1, (t.keys + kKeys - 1) / kKeys);
+        t.t = (int)(r / t.units);
+        r -= (long long)t.t * t.units;
+    } else {
+        const int tiles = (t.q.n * a.group + kRows - 1) / kRows;
+        for (t.t = 0;; ++t.t) {
+            t.keys = tile_keys(t.q, a.group, t.t * kRows, kRows, true);
+            t.units = max(1, (t.keys + kKeys - 1) / kKeys);
+            if (r < t.units || t.t + 1 >= tiles) break;
+            r -= t.units;
+        }
+    }
+    t.u0 = (int)r;
+    t.n = max(1, (int)min((long long)(t.units - t.u0), left));
+    return t;
+}
+
+// The tile after `t` in the list.
+template <int kRows, int kKeys>
+__device__ __forceinline__ void next_tile(const AttnArgs& a, const WorkList& w, Tile& t, long long left) {
+    const int tiles = (t.q.n * a.group + kRows - 1) / kRows;
+    if (++t.t == tiles) {
+        t.t = 0;
+        if (++t.head == a.kv.n_kv) {
+            t.head = 0;
+            do ++t.s;
+            while (t.s + 1 < a.b.n_seq && w.prefix[t.s + 1] == w.prefix[t.s]);
+            t.s = min(t.s, a.b.n_seq - 1);
+            t.q = load_seq(a.b, a.kv.page_shift, t.s);
+        }
+    }
+    t.keys = tile_keys(t.q, a.group, t.t * kRows, kRows, a.causal);
+    t.units = max(1, (t.keys + kKeys - 1) / kKeys);
+    t.u0 = 0;
+    t.n = (int)min((long long)t.units, left);
+}
+
+// Last position packed row i of a sequence sees.
+__device__ __forceinline__ int row_limit(const AttnArgs& a, const Seq& q, int i) {
+    return a.causal ? q.kv - q.n + i / a.group : q.kv - 1;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+}  // namespace paged
+}  // namespace qwen2

@@ -1,0 +1,719 @@
+// Attention over the paged cache for few new rows per sequence (single
+// tokens, speculated tokens, short chunks), and the join of partial tiles.
+//
+//   o_i = sum_j w_ij v_j / sum_j w_ij,   w_ij = 2^(s_ij - m_i),
+//   s_ij = scale log2(e) q_i . k_j,      m_i = max_j s_ij,
+//
+// taken in one pass over the keys with the running maximum and sum of each
+// row (online softmax).  Bound by HBM: every cached byte is read once, for
+// group * rows products of 2 hd flops, far below the tensor cores' rate.
+//
+// Split (paged.cuh): a tile is up to kRows = 16 MT packed rows of one kv head,
+// a unit 64 positions.  Inside a CTA warp w takes positions 16 w .. 16 w + 15
+// of every unit on its own: its loads, softmax statistics and accumulators
+// are the warp's, so the main loop has no block barrier.  The four warps meet
+// at a tile's end in shared memory.  16 positions never cross a page, so a
+// step needs one page lookup, loaded a step before its copies are issued.
+//
+// Loads: cp.async in 16-byte pieces, kStages steps in flight per warp, and
+// positions past the tile's keys are filled with zeros instead of read (what
+// a page holds there may be NaN).  Products: mma m16n8k16, the rows in M and
+// the positions (scores) or dims (values) in N.
+//
+// 8-bit pages: codes become exact f16 in registers (int8: 1024 + (c + 128)
+// by a byte permute, minus 1152; e4m3: the hardware conversion) and the f32
+// scales stay out of the products: the scores are multiplied by k's scale,
+// the probabilities by v's, relative to G, the warp's largest v scale so far
+// rounded up to a power of two, which the accumulators carry like the running
+// maximum (f16 would lose small scales otherwise).  bf16 queries over 8-bit
+// pages enter as f16 scaled by a power of two of their row's largest
+// magnitude, which the scores are multiplied back by: exact but for dims
+// below 2^-24 of the row's largest.
+#include <cuda_fp8.h>
+
+#include "paged.cuh"
+#include "paged.h"
+
+namespace qwen2 {
+namespace paged {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnit = 64;      // positions per unit
+constexpr int kStep = 16;      // positions per warp and unit
+
+enum Kind { kSame16, kInt8, kE4m3 };
+
+template <int HD, Kind K>
+struct Shape {
+    static constexpr int kSize = K == kSame16 ? 2 : 1;
+    static constexpr int kRowBytes = HD * kSize;                   // one position of one head
+    static constexpr int kTile = kStep * kRowBytes;                // K or V of a step
+    static constexpr int kScales = K == kSame16 ? 0 : 2 * kStep * 4;
+    static constexpr int kStage = 2 * kTile + kScales;
+    static constexpr int kStages = kTile <= 1024 ? 6 : kTile <= 2048 ? 4 : 3;
+    static constexpr int kRing = kStage * kStages;                 // per warp
+};
+
+template <int HD, int MT>
+struct Meet {   // where the warps meet
+    float o[16 * MT][HD + 4];
+    float m[kWarps][16 * MT], l[kWarps][16 * MT], g[kWarps];
+};
+
+// 16-byte piece c of position r stands at piece c ^ f(r) of its row, so that
+// both 8 rows' pieces of one column (ldmatrix) and 4 pieces of two adjacent
+// rows (8-bit K) fall into all banks.
+template <int RB>
+__device__ __forceinline__ int swz(int r, int c) {
+    if constexpr (RB == 64) return c ^ ((r >> 1) & 3);
+    else return c ^ (((r & 1) << 2) | ((r >> 1) & 3));
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool full) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(full ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+// Two codes of `w`, bytes (0,1) or (2,3) for FIRST = 0 / 2 and STEP = 1, bytes
+// (0,2) or (1,3) for FIRST = 0 / 1 and STEP = 2, as exact f16.
+template <Kind K, int FIRST, int STEP>
+__device__ __forceinline__ uint32_t codes2(uint32_t w) {
+    if constexpr (K == kInt8) {
+        constexpr int sel = 0x4040 | FIRST | (FIRST + STEP) << 8;
+        const uint32_t h = __byte_perm(w ^ 0x80808080u, 0x64646464u, sel);
+        const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x6480)));
+        return *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+        constexpr int sel = 0x4400 | FIRST | (FIRST + STEP) << 4;
+        const uint32_t p = STEP == 1 && FIRST == 0 ? w : __byte_perm(w, 0, sel);
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)p, __NV_E4M3);
+        return (uint32_t)h.x | (uint32_t)h.y << 16;
+    }
+}
+
+__device__ __forceinline__ float quad_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    return v + __shfl_xor_sync(0xffffffffu, v, 2);
+}
+
+// The power of two at or above v, as an exponent in [-100, 100].
+__device__ __forceinline__ int ceil_log2(float v) {
+    const int b = __float_as_int(v);
+    const int e = ((b >> 23) & 255) - 127 + ((b & 0x7fffff) != 0);
+    return min(max(e, -100), 100);
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+__device__ __forceinline__ void store_part_none(const Parts& p, int slot) {
+    if (threadIdx.x == 0) p.info[slot].state = kPartNone;
+}
+
+// The copies of one warp step: cursor over the CTA's units, `ahead` steps
+// before the products.
+struct Feed {
+    Tile t;
+    int i;                 // unit within the tile's part
+    long long left;        // units of the CTA not yet handed out, this tile's included
+};
+
+template <int HD, Kind K, bool BF16, int MT>
+__global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__ AttnArgs a) {
+    using S = Shape<HD, K>;
+    constexpr bool k8 = K != kSame16;
+    constexpr bool kMmaBf16 = BF16 && !k8;
+    constexpr int kRows = 16 * MT;
+    constexpr int RB = S::kRowBytes;
+    extern __shared__ __align__(128) unsigned char smem[];
+    Meet<HD, MT>& meet = *reinterpret_cast<Meet<HD, MT>*>(smem);
+    unsigned char* rings = smem + (sizeof(Meet<HD, MT>) + 127) / 128 * 128;
+    long long* prefix = reinterpret_cast<long long*>(rings + kWarps * S::kRing);
+
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t4 = lane & 3;
+    const WorkList work = build_work<kRows, kUnit>(a, prefix, 1);
+    const int slot0 = 2 * blockIdx.x;
+    bool wrote0 = false, wrote1 = false;
+    long long left = work.end - work.begin;
+    if (left > 0) {
+        const uint32_t ring = (uint32_t)__cvta_generic_to_shared(rings + warp * S::kRing);
+        Tile t = find_tile<kRows, kUnit>(a, work, work.begin, left);
+        Feed f{t, 0, left};
+        int f_page = -1;
+        // Page of the feed's current step; -1 if it has no keys, -2 if its id is bad.
+        auto look_up = [&]() -> int {
+            if (f.left <= 0) return -1;
+            const int key0 = (f.t.u0 + f.i) * kUnit + warp * kStep;
+            if (key0 >= f.t.keys) return -1;
+            const int p = __ldg(a.b.pages + (long long)f.t.s * a.b.pages_stride + (key0 >> a.kv.page_shift));
+            return (unsigned)p < (unsigned)a.kv.n_pages ? p : -2;
+        };
+        unsigned bad = 0;     // per ring stage: its page id was bad
+        // Issues the copies of the feed's step into `stage` and moves it on.
+        auto issue = [&](int stage) {
+            bad &= ~(1u << stage);
+            if (f_page >= 0) {
+                const int key0 = (f.t.u0 + f.i) * kUnit + warp * kStep;
+                const int off = key0 & ((1 << a.kv.page_shift) - 1);
+                const int n = f.t.keys - key0;       // positions of the step that are keys
+                const long long at = (long long)f_page * a.kv.page_bytes + (long long)off * a.kv.token_bytes +
+                                     (long long)f.t.head * a.kv.head_bytes;
+                const uint32_t dst = ring + stage * S::kStage;
+#pragma unroll
+                for (int i = 0; i < RB / 32; ++i) {
+                    const int e = lane + 32 * i, r = e / (RB / 16), c = e % (RB / 16);
+                    const bool in = r < n;
+                    const long long src = at + (long long)(in ? r : 0) * a.kv.token_bytes + 16 * c;
+                    const uint32_t d = dst + r * RB + 16 * swz<RB>(r, c);
+                    cp16(d, a.kv.k + src, in);
+                    cp16(d + S::kTile, a.kv.v + src, in);
+                }
+                if constexpr (k8) {
+                    if (lane < 8) {
+                        const int c = lane & 3;
+                        const float* sc = (lane < 4 ? a.kv.k_scale : a.kv.v_scale) +
+                                          (((long long)f_page * a.kv.n_kv + f.t.head) << a.kv.page_shift) + off;
+                        cp16(dst + 2 * S::kTile + 16 * lane, sc + 4 * c, true);
+                    }
+                }
+            } else if (f_page == -2) {
+                bad |= 1u << stage;
+                if (lane == 0) raise_guard(a.b.guard, QWEN2_GUARD_PAGE);
+            }
+            cp_commit();
+            if (f.left > 0) {
+                --f.left;
+                if (++f.i == f.t.n) {
+                    f.i = 0;
+                    if (f.left > 0) next_tile<kRows, kUnit>(a, work, f.t, f.left);
+                }
+            }
+            f_page = look_up();
+        };
+        f_page = look_up();
+#pragma unroll 1
+        for (int st = 0; st < S::kStages - 1; ++st) issue(st);
+        int stage = 0;
+
+        for (;;) {
+            // ---- a tile's part: queries ------------------------------------------
+            const int packed0 = t.t * kRows, packed = t.q.n * a.group;
+            uint32_t qf[MT][HD / 16][4];
+            float rs[MT][2];           // factor of a row's scores
+            int lim[MT][2];            // last position a row sees
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int i = packed0 + 16 * mt + 8 * h + g;
+                    const bool in = i < packed;
+                    const int row = t.q.q0 + (in ? i / a.group : 0), qh = t.head * a.group + (in ? i % a.group : 0);
+                    const char* src = a.q.data + (long long)row * a.q.row_bytes + (long long)qh * a.q.head_bytes;
+                    lim[mt][h] = in ? row_limit(a, t.q, i) : 0x7fffffff;
+                    rs[mt][h] = a.scale_log2;
+                    if constexpr (!k8) {
+#pragma unroll
+                        for (int k = 0; k < HD / 16; ++k) {
+                            qf[mt][k][h] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + 32 * k + 4 * t4)) : 0u;
+                            qf[mt][k][2 + h] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + 32 * k + 16 + 4 * t4)) : 0u;
+                        }
+                    } else {
+                        // Dims in the order the codes are read in: 4 codes of a word
+                        // make the two halves of a k step's pairs.
+                        uint4 w[HD / 32];
+#pragma unroll
+                        for (int b = 0; b < HD / 64; ++b)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                w[2 * b + j] = in ? __ldg(reinterpret_cast<const uint4*>(src + 128 * b + 32 * t4 + 16 * j))
+                                                  : make_uint4(0, 0, 0, 0);
+                        if constexpr (BF16) {
+                            float big = 0.f;
+                            float x[HD / 4];
+#pragma unroll
+                            for (int j = 0; j < HD / 32; ++j) {
+                                const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    x[8 * j + 2 * e] = __uint_as_float(u[e] << 16);
+                                    x[8 * j + 2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+                                    big = fmaxf(big, fmaxf(fabsf(x[8 * j + 2 * e]), fabsf(x[8 * j + 2 * e + 1])));
+                                }
+                            }
+                            const int e2 = ceil_log2(quad_max(big));
+                            const float down = pow2i(-e2);
+                            rs[mt][h] *= pow2i(e2);
+#pragma unroll
+                            for (int j = 0; j < HD / 32; ++j)
+                                w[j] = make_uint4(pack2<false>(x[8 * j] * down, x[8 * j + 1] * down),
+                                                  pack2<false>(x[8 * j + 2] * down, x[8 * j + 3] * down),
+                                                  pack2<false>(x[8 * j + 4] * down, x[8 * j + 5] * down),
+                                                  pack2<false>(x[8 * j + 6] * down, x[8 * j + 7] * down));
+                        }
+#pragma unroll
+                        for (int j = 0; j < HD / 32; ++j) {
+                            qf[mt][2 * j][h] = w[j].x;
+                            qf[mt][2 * j][2 + h] = w[j].y;
+                            qf[mt][2 * j + 1][h] = w[j].z;
+                            qf[mt][2 * j + 1][2 + h] = w[j].w;
+                        }
+                    }
+                }
+            const int sure = row_limit(a, t.q, packed0);   // every row of the tile sees positions up to here
+            float o[MT][HD / 8][4];
+            float m[MT][2], l[MT][2];
+            int ge = -100;             // exponent of G
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[mt][d][e] = 0.f;
+                m[mt][0] = m[mt][1] = -INFINITY;
+                l[mt][0] = l[mt][1] = 0.f;
+            }
+            // ---- its units --------------------------------------------------------
+            for (int i = 0; i < t.n; ++i) {
+                cp_wait<S::kStages - 2>();
+                __syncwarp();
+                // The stage that the step before this one emptied is filled again.
+                issue(stage == 0 ? S::kStages - 1 : stage - 1);
+                const int key0 = (t.u0 + i) * kUnit + warp * kStep;
+                const uint32_t kt = ring + stage * S::kStage, vt = kt + S::kTile;
+                const bool skip = key0 >= t.keys || (bad >> stage & 1);
+                if (!skip) {
+                    // scores
+                    float s[MT][2][4];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+                    if constexpr (!k8) {
+                        const int r = (lane & 7) + ((lane >> 4) << 3), c = (lane >> 3) & 1;
+#pragma unroll
+                        for (int k = 0; k < HD / 16; ++k) {
+                            uint32_t b[4];
+                            ldsm4(kt + r * RB + 16 * swz<RB>(r, 2 * k + c), b);
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                mma16816<kMmaBf16>(s[mt][0], qf[mt][k], b[0], b[1]);
+                                mma16816<kMmaBf16>(s[mt][1], qf[mt][k], b[2], b[3]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                            for (int b = 0; b < HD / 64; ++b) {
+                                const int r = 8 * nt + g;
+                                uint32_t w[4];
+                                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                             : "r"(kt + r * RB + 16 * swz<RB>(r, 4 * b + t4))
+                                             : "memory");
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const uint32_t b0 = codes2<K, 0, 1>(w[k]), b1 = codes2<K, 2, 1>(w[k]);
+#pragma unroll
+                                    for (int mt = 0; mt < MT; ++mt)
+                                        mma16816<false>(s[mt][nt], qf[mt][4 * b + k], b0, b1);
+                                }
+                            }
+                    }
+                    // scales, mask, running maximum
+                    float vs[2][2];        // v's scale of positions (nt, pair) relative to G
+                    float vscale[2][2];
+                    if constexpr (k8) {
+                        float top = 0.f;
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt) {
+                            float2 ks, vv;
+                            const uint32_t sa = kt + 2 * S::kTile + 4 * (8 * nt + 2 * t4);
+                            asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(ks.x), "=f"(ks.y) : "r"(sa) : "memory");
+                            asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(vv.x), "=f"(vv.y) : "r"(sa + 64) : "memory");
+                            // Positions that are no keys: whatever stands in the pool there is left out.
+                            const int j = key0 + 8 * nt + 2 * t4;
+                            vscale[nt][0] = j < t.keys ? vv.x : 0.f;
+                            vscale[nt][1] = j + 1 < t.keys ? vv.y : 0.f;
+                            top = fmaxf(top, fmaxf(vscale[nt][0], vscale[nt][1]));
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                s[mt][nt][0] *= ks.x;
+                                s[mt][nt][1] *= ks.y;
+                                s[mt][nt][2] *= ks.x;
+                                s[mt][nt][3] *= ks.y;
+                            }
+                        }
+                        const int ne = max(ge, ceil_log2(quad_max(top)));
+                        if (ne != ge) {
+                            const float down = pow2i(max(ge - ne, -126));
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                                for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) o[mt][d][e] *= down;
+                            ge = ne;
+                        }
+                        const float inv = pow2i(-ge);
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt) {
+                            vs[nt][0] = vscale[nt][0] * inv;
+                            vs[nt][1] = vscale[nt][1] * inv;
+                        }
+                    }
+                    const bool cut = key0 + kStep - 1 > sure || key0 + kStep > t.keys;
+                    uint32_t p[MT][4];
+                    bool moved = false;
+                    float corr[MT][2];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float v[4] = {s[mt][0][2 * h] * rs[mt][h], s[mt][0][2 * h + 1] * rs[mt][h],
+                                          s[mt][1][2 * h] * rs[mt][h], s[mt][1][2 * h + 1] * rs[mt][h]};
+                            if (cut) {
+                                const int last = min(lim[mt][h], t.keys - 1);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (key0 + 8 * (e >> 1) + 2 * t4 + (e & 1) > last) v[e] = -INFINITY;
+                            }
+                            const float mx = quad_max(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+                            const float mn = fmaxf(m[mt][h], mx);
+                            const float base = mn == -INFINITY ? 0.f : mn;
+                            moved |= mn != m[mt][h];
+                            corr[mt][h] = ex2(m[mt][h] - base);
+                            m[mt][h] = mn;
+                            float sum = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                v[e] = ex2(v[e] - base);
+                                sum += v[e];
+                            }
+                            l[mt][h] = fmaf(l[mt][h], corr[mt][h], sum);
+                            if constexpr (k8) {
+                                v[0] *= vs[0][0];
+                                v[1] *= vs[0][1];
+                                v[2] *= vs[1][0];
+                                v[3] *= vs[1][1];
+                            }
+                            p[mt][h] = pack2<kMmaBf16>(v[0], v[1]);
+                            p[mt][2 + h] = pack2<kMmaBf16>(v[2], v[3]);
+                        }
+                    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                            for (int d = 0; d < HD / 8; ++d) {
+                                o[mt][d][0] *= corr[mt][0];
+                                o[mt][d][1] *= corr[mt][0];
+                                o[mt][d][2] *= corr[mt][1];
+                                o[mt][d][3] *= corr[mt][1];
+                            }
+                    }
+                    // values
+                    const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
+#pragma unroll
+                    for (int d = 0; d < RB / 32; ++d) {
+                        uint32_t b[4];
+                        ldsm4t(vt + r * RB + 16 * swz<RB>(r, 2 * d + c), b);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            if constexpr (!k8) {
+                                mma16816<kMmaBf16>(o[mt][2 * d], p[mt], b[0], b[1]);
+                                mma16816<kMmaBf16>(o[mt][2 * d + 1], p[mt], b[2], b[3]);
+                            } else {
+                                // A piece is 16 dims: the even ones make one n tile, the odd ones another.
+                                mma16816<false>(o[mt][4 * d], p[mt], codes2<K, 0, 2>(b[0]), codes2<K, 0, 2>(b[1]));
+                                mma16816<false>(o[mt][4 * d + 1], p[mt], codes2<K, 1, 2>(b[0]), codes2<K, 1, 2>(b[1]));
+                                mma16816<false>(o[mt][4 * d + 2], p[mt], codes2<K, 0, 2>(b[2]), codes2<K, 0, 2>(b[3]));
+                                mma16816<false>(o[mt][4 * d + 3], p[mt], codes2<K, 1, 2>(b[2]), codes2<K, 1, 2>(b[3]));
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                stage = stage + 1 == S::kStages ? 0 : stage + 1;
+            }
+            // ---- the four warps meet ----------------------------------------------
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float sum = quad_sum(l[mt][h]);
+                    if (t4 == 0) {
+                        meet.m[warp][16 * mt + 8 * h + g] = m[mt][h];
+                        meet.l[warp][16 * mt + 8 * h + g] = sum;
+                    }
+                }
+            __syncthreads();
+            float f_row[MT][2];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, meet.m[w][16 * mt + 8 * h + g]);
+                    f_row[mt][h] = ex2(m[mt][h] - (top == -INFINITY ? 0.f : top));
+                    if constexpr (k8) f_row[mt][h] *= pow2i(ge);
+                }
+#pragma unroll 1
+            for (int w = 0; w < kWarps; ++w) {
+                if (warp == w) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int d = 0; d < HD / 8; ++d)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int h = e >> 1, r = 16 * mt + 8 * h + g;
+                                const int col = k8 ? 16 * (d >> 1) + 4 * t4 + 2 * (e & 1) + (d & 1)
+                                                   : 8 * d + 2 * t4 + (e & 1);
+                                const float x = o[mt][d][e] * f_row[mt][h];
+                                if (w == 0) meet.o[r][col] = x;
+                                else meet.o[r][col] += x;
+                            }
+                }
+                __syncthreads();
+            }
+            // ---- out: finished rows, or a partial ------------------------------------
+            const bool begins = t.u0 == 0, ends = t.u0 + t.n >= t.units;
+            const int slot = slot0 + (begins ? 1 : 0);
+            const bool whole = begins && ends;
+            if (!whole) {
+                if (begins) wrote1 = true;
+                else wrote0 = true;
+                if (threadIdx.x == 0) {
+                    PartInfo pi;
+                    pi.q0 = t.q.q0;
+                    pi.packed0 = packed0;
+                    pi.packed_end = min(packed0 + kRows, packed);
+                    pi.head = t.head;
+                    pi.state = kPartUsed | (ends ? kPartLast : 0);
+                    a.parts.info[slot] = pi;
+                }
+            }
+            for (int e = threadIdx.x; e < kRows * (HD / 8); e += kThreads) {
+                const int r = e / (HD / 8), c = e % (HD / 8);
+                const int i = packed0 + r;
+                if (i >= packed) continue;
+                float top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, meet.m[w][r]);
+                const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) sum += meet.l[w][r] * ex2(meet.m[w][r] - base);
+                const float4 x0 = *reinterpret_cast<const float4*>(&meet.o[r][8 * c]);
+                const float4 x1 = *reinterpret_cast<const float4*>(&meet.o[r][8 * c + 4]);
+                if (whole) {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                    const int row = t.q.q0 + i / a.group, qh = t.head * a.group + i % a.group;
+                    *reinterpret_cast<uint4*>(a.out.data + (long long)row * a.out.row_bytes +
+                                              (long long)qh * a.out.head_bytes + 16 * c) =
+                        make_uint4(pack2<BF16>(x0.x * inv, x0.y * inv), pack2<BF16>(x0.z * inv, x0.w * inv),
+                                   pack2<BF16>(x1.x * inv, x1.y * inv), pack2<BF16>(x1.z * inv, x1.w * inv));
+                    if (a.lse && c == 0)
+                        a.lse[(long long)row * a.n_head + qh] =
+                            sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+                } else {
+                    float* po = a.parts.o + ((long long)slot * kRows + r) * HD + 8 * c;
+                    reinterpret_cast<float4*>(po)[0] = x0;
+                    reinterpret_cast<float4*>(po)[1] = x1;
+                    if (c == 0) {
+                        a.parts.ml[(long long)slot * 2 * kRows + r] = top;
+                        a.parts.ml[(long long)slot * 2 * kRows + kRows + r] = sum;
+                    }
+                }
+            }
+            __syncthreads();
+            left -= t.n;
+            if (left <= 0) break;
+            next_tile<kRows, kUnit>(a, work, t, left);
+        }
+        cp_wait<0>();
+    }
+    if (!wrote0) store_part_none(a.parts, slot0);
+    if (!wrote1) store_part_none(a.parts, slot0 + 1);
+}
+
+// Adds up the tile that begins in CTA blockIdx.x's slot 1 and goes on in the
+// slots 0 of the CTAs after it: rows blockIdx.y, blockIdx.y + gridDim.y, ...
+// of it, a block per row, its warps taking the parts in turn.
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ AttnArgs a, int n_cta) {
+    constexpr int kV = HD / 32;     // dims per lane
+    __shared__ float so[4][HD], sl[4];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int c0 = blockIdx.x;
+    const PartInfo first = a.parts.info[2 * c0 + 1];
+    if (first.state == kPartNone) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows = a.parts.rows;
+    // Parts: slot 2 c0 + 1, then slots 2 c of the following CTAs up to the last.
+    int n = 1;
+    for (int c = c0 + 1;; ++n, ++c) {
+        if (c >= n_cta) break;
+        const int st = a.parts.info[2 * c].state;
+        if (st == kPartNone) break;
+        if (st & kPartLast) {
+            ++n;
+            break;
+        }
+    }
+    for (int r = blockIdx.y; first.packed0 + r < first.packed_end; r += gridDim.y) {
+        const auto slot = [&](int k) { return k == 0 ? 2 * c0 + 1 : 2 * (c0 + k); };
+        float top = -INFINITY;
+        for (int k = lane; k < n; k += 32) top = fmaxf(top, a.parts.ml[(long long)slot(k) * 2 * rows + r]);
+        top = warp_max(top);
+        const float base = top == -INFINITY ? 0.f : top;
+        float acc[kV], sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int k = warp; k < n; k += 4) {
+            const float* ml = a.parts.ml + (long long)slot(k) * 2 * rows + r;
+            const float w = ex2(ml[0] - base);
+            sum = fmaf(ml[rows], w, sum);
+            const float* o = a.parts.o + ((long long)slot(k) * rows + r) * HD + kV * lane;
+#pragma unroll
+            for (int e = 0; e < kV; ++e) acc[e] = fmaf(o[e], w, acc[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < kV; ++e) so[warp][kV * lane + e] = acc[e];
+        if (lane == 0) sl[warp] = sum;
+        __syncthreads();
+        const int i = first.packed0 + r;
+        const int row = first.q0 + i / a.group, qh = first.head * a.group + i % a.group;
+        sum = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (threadIdx.x < HD / 2) {
+            const int d = 2 * threadIdx.x;
+            const float x = ((so[0][d] + so[1][d]) + (so[2][d] + so[3][d])) * inv;
+            const float y = ((so[0][d + 1] + so[1][d + 1]) + (so[2][d + 1] + so[3][d + 1])) * inv;
+            *reinterpret_cast<uint32_t*>(a.out.data + (long long)row * a.out.row_bytes +
+                                         (long long)qh * a.out.head_bytes + 4 * threadIdx.x) = pack2<BF16>(x, y);
+        }
+        if (a.lse && threadIdx.x == 0)
+            a.lse[(long long)row * a.n_head + qh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        __syncthreads();
+    }
+}
+
+// CTAs of the few-rows kernel: as many as stay resident (registers allow 3 an
+// SM with 16 rows and 2 with 32; shared memory may allow fewer).
+constexpr int kMaxCtasPerSm = 3;
+
+template <int HD, Kind K, bool BF16, int MT>
+cudaError_t launch_few(AttnArgs a, int n_sm, cudaStream_t st) {
+    using S = Shape<HD, K>;
+    const size_t smem = (sizeof(Meet<HD, MT>) + 127) / 128 * 128 + kWarps * S::kRing + 8 * ((size_t)a.b.n_seq + 1);
+    auto kern = k_paged_attn<HD, K, BF16, MT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    const int by_smem = (int)(228 * 1024 / (smem + 1024));
+    const int grid = n_sm * max(1, min(by_smem, MT == 1 ? kMaxCtasPerSm : 2));
+    a.parts = carve_parts(a.parts.info, grid, 16 * MT);
+    kern<<<grid, kThreads, smem, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_attn_join<HD, BF16>, dim3(grid, 16), dim3(128), 0, st, a, grid);
+}
+
+template <int HD, Kind K, bool BF16>
+cudaError_t launch_rows(const AttnArgs& a, int mt, int n_sm, cudaStream_t st) {
+    return mt == 1 ? launch_few<HD, K, BF16, 1>(a, n_sm, st) : launch_few<HD, K, BF16, 2>(a, n_sm, st);
+}
+
+template <int HD, bool BF16>
+cudaError_t launch_kind(const AttnArgs& a, int format, int mt, int n_sm, cudaStream_t st) {
+    if (format == QWEN2_KV_INT8) return launch_rows<HD, kInt8, BF16>(a, mt, n_sm, st);
+    if (format == QWEN2_KV_E4M3) return launch_rows<HD, kE4m3, BF16>(a, mt, n_sm, st);
+    return launch_rows<HD, kSame16, BF16>(a, mt, n_sm, st);
+}
+
+}  // namespace
+
+long long attn_workspace(const Batch& b, const Pool& kv, int head_dim, int n_head, int n_sm) {
+    const int group = n_head / kv.n_kv;
+    return parts_bytes(n_sm * kMaxCtasPerSm, (long long)b.max_q * group <= 16 ? 16 : 32, head_dim);
+}
+
+cudaError_t enqueue_attention(const Pool& kv, const Batch& b, const AttnCall& c, const Rows& q, const Rows& out,
+                              int n_sm, cudaStream_t st) {
+    AttnArgs a{};
+    a.kv = kv;
+    a.b = b;
+    a.q = q;
+    a.out = out;
+    a.lse = c.lse;
+    a.n_head = c.n_head;
+    a.group = c.n_head / kv.n_kv;
+    a.causal = c.causal;
+    a.scale_log2 = c.scale * 1.4426950408889634f;
+    a.rows_lo = 0;
+    a.rows_hi = 0x7fffffff;
+    const int mt = (long long)b.max_q * a.group <= 16 ? 1 : 2;
+    a.parts.info = static_cast<PartInfo*>(c.workspace);
+    if (c.head_dim == 64)
+        return c.dtype == QWEN2_DTYPE_BF16 ? launch_kind<64, true>(a, c.format, mt, n_sm, st)
+                                           : launch_kind<64, false>(a, c.format, mt, n_sm, st);
+    return c.dtype == QWEN2_DTYPE_BF16 ? launch_kind<128, true>(a, c.format, mt, n_sm, st)
+                                       : launch_kind<128, false>(a, c.format, mt, n_sm, st);
+}
+
+}  // namespace paged
+}  // namespace qwen2

@@ -1,0 +1,468 @@
+// The row-wise operators of the paged key / value cache:
+//
+// k_paged_write: projected rows to finished queries and cache pages in one
+// pass.  Per head of hd dims:  y = x / sqrt(mean(x^2) + eps) * w (optional),
+// the first R dims turned by the row's (cos, sin), then q -> 16 bits, k and
+// v -> the pages' format.  An 8-bit head keeps one f32 scale s = max|y| / L
+// (L = 127 or 448; 1 for a head of zeros) and codes of y / s.
+//
+// k_paged_read: pages to contiguous rows.
+//
+// Both are bound by HBM traffic (a dozen flops an element): every element is
+// read once and written once, in 16-byte pieces.  A head of hd dims is the
+// work of hd / 8 lanes, 8 dims each (k_paged_read: 16 codes each for 8-bit
+// pages), so the norm's sum, the largest magnitude and the rotation's
+// partner dims are a few shuffles inside one warp.
+#include <cuda_fp8.h>
+
+#include "paged.cuh"
+#include "paged.h"
+
+namespace qwen2 {
+namespace paged {
+
+namespace {
+
+constexpr int kRowThreads = 256;
+
+// Eight elements of a row as f32.
+template <int DT>
+__device__ __forceinline__ void load8(const char* p, float (&x)[8]) {
+    if constexpr (DT == QWEN2_DTYPE_F32) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 f;
+            if constexpr (DT == QWEN2_DTYPE_F16) f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, bool bf16) {
+    if (bf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ uint4 pack8_16(const float (&x)[8], bool bf16) {
+    return make_uint4(pack2(x[0], x[1], bf16), pack2(x[2], x[3], bf16), pack2(x[4], x[5], bf16),
+                      pack2(x[6], x[7], bf16));
+}
+
+// max that keeps a NaN, so that a head holding one gets a NaN scale instead
+// of losing it.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t int8_code(float y) {
+    // Half away from zero, as the weights' Q8_0 blocks are rounded.
+    return (uint32_t)(uint8_t)(int8_t)fminf(fmaxf(roundf(y), -127.f), 127.f);
+}
+
+// Eight 8-bit codes of x / scale.
+template <int FMT>
+__device__ __forceinline__ uint2 pack8_8(const float (&x)[8], float scale) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = __fdiv_rn(x[4 * i + j], scale);
+        if constexpr (FMT == QWEN2_KV_INT8) {
+            w[i] = int8_code(y[0]) | int8_code(y[1]) << 8 | int8_code(y[2]) << 16 | int8_code(y[3]) << 24;
+        } else {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+            w[i] = lo | hi << 16;
+        }
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// The sequence that holds `row`: the number of sequences that end at or before
+// it.  Up to 256 sequences are counted by the warp's lanes, all loads in
+// flight at once; more go by bisection.  `start` is ascending; if it is not,
+// the result is still inside [0, n_seq].
+__device__ __forceinline__ int find_seq(const int* start, int n_seq, int row, int lane) {
+    if (n_seq <= 256) {
+        int c = 0;
+        for (int i = 1 + lane; i <= n_seq; i += 32) c += __ldg(start + i) <= row;
+        return __reduce_add_sync(0xffffffffu, c);
+    }
+    int lo = 0, hi = n_seq;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(start + mid + 1) <= row) lo = mid + 1;
+        else hi = mid;
+    }
+    return lo;
+}
+
+struct WriteArgs {
+    Pool kv;
+    Batch b;
+    Rows q, q_out, k, v;
+    const float *q_norm, *k_norm;
+    const float* rope;
+    float eps;
+    int rope_rows, rotary, interleaved;
+    int n_head;         // 0: no queries
+    int slices;         // warps one row's heads are spread over
+    int out_bf16;
+};
+
+// One warp per (row, slice of its heads): a row's lookups and rotation factors
+// are loaded once and serve all its heads.
+template <int DT, int FMT, int HD>
+__global__ void __launch_bounds__(kRowThreads) k_paged_write(const __grid_constant__ WriteArgs a) {
+    constexpr int kLanes = HD / 8;            // lanes per head
+    constexpr int kHeads = 32 / kLanes;       // heads per warp step
+    constexpr int kIn = DT == QWEN2_DTYPE_F32 ? 4 : 2;
+    const int lane = threadIdx.x & 31;
+    const long long w = (long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+    const long long row_l = w / a.slices;
+    if (row_l >= a.b.n_rows) return;
+    const int row = (int)row_l, slice = (int)(w - row_l * a.slices);
+    const int s = find_seq(a.b.q_start, a.b.n_seq, row, lane);
+    if (s >= a.b.n_seq) return;
+    const Seq q = load_seq(a.b, a.kv.page_shift, s);
+    if (q.bad_rows || q.bad_len) {
+        if (lane == 0) raise_guard(a.b.guard, q.bad_rows ? kGuardShape : kGuardPosition);
+        return;
+    }
+    const int i = row - q.q0;
+    if (i < 0 || i >= q.n) return;            // not this sequence's: q_start is not ascending, or row < q_start[0]
+    const int pos = q.kv - q.n + i;
+    if (pos < 0 || (a.rotary && pos >= a.rope_rows)) {
+        if (lane == 0) raise_guard(a.b.guard, kGuardPosition);
+        return;
+    }
+    const int page = __ldg(a.b.pages + (long long)s * a.b.pages_stride + (pos >> a.kv.page_shift));
+    if ((unsigned)page >= (unsigned)a.kv.n_pages) {
+        if (lane == 0) raise_guard(a.b.guard, QWEN2_GUARD_PAGE);
+        return;
+    }
+    const int off = pos & ((1 << a.kv.page_shift) - 1);
+    const int c = lane % kLanes, sub = lane / kLanes;
+
+    // This lane's 8 dims' rotation factors: turned[e] = x[e] * cs[e] + partner[e] * sn[e].
+    float cs[8], sn[8];
+    int partner = lane;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        cs[e] = 1.f;
+        sn[e] = 0.f;
+    }
+    const bool turns = 8 * c < a.rotary;
+    if (turns) {
+        const float* t = a.rope + (long long)pos * a.rotary;
+        if (a.interleaved) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const float4 f = __ldg(reinterpret_cast<const float4*>(t + 8 * c) + p);
+                cs[4 * p] = cs[4 * p + 1] = f.x;
+                sn[4 * p] = -f.y;
+                sn[4 * p + 1] = f.y;
+                cs[4 * p + 2] = cs[4 * p + 3] = f.z;
+                sn[4 * p + 2] = -f.w;
+                sn[4 * p + 3] = f.w;
+            }
+        } else {
+            const int half = a.rotary >> 4;   // lanes of half the turning dims
+            const bool hi = c >= half;
+            const float4* f4 = reinterpret_cast<const float4*>(t + 16 * (hi ? c - half : c));
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float4 f = __ldg(f4 + p);
+                cs[2 * p] = f.x;
+                sn[2 * p] = hi ? f.y : -f.y;
+                cs[2 * p + 1] = f.z;
+                sn[2 * p + 1] = hi ? f.w : -f.w;
+            }
+            partner = hi ? lane - half : lane + half;
+        }
+    }
+    const int n_slots = a.n_head + 2 * a.kv.n_kv;
+    // Steps of kHeads heads; every lane of the warp takes every step.
+    for (int h0 = slice * kHeads; h0 < n_slots; h0 += a.slices * kHeads) {
+        const int slot = h0 + sub;
+        const bool live = slot < n_slots;
+        const int kind = slot < a.n_head ? 0 : slot < a.n_head + a.kv.n_kv ? 1 : 2;   // q, k, v
+        const int h = kind == 0 ? slot : kind == 1 ? slot - a.n_head : slot - a.n_head - a.kv.n_kv;
+        const Rows& src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        if (live) load8<DT>(src.data + (long long)row * src.row_bytes + (long long)h * src.head_bytes + 8 * kIn * c, x);
+        const float* nw = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
+        if (a.q_norm || a.k_norm) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (nw) {
+                const float r = rms_scale(ss, HD, a.eps);
+                const float4 w0 = __ldg(reinterpret_cast<const float4*>(nw + 8 * c));
+                const float4 w1 = __ldg(reinterpret_cast<const float4*>(nw + 8 * c) + 1);
+                const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = x[e] * r * wv[e];
+            }
+        }
+        if (a.rotary) {
+            float p[8];
+            if (a.interleaved) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, x[e], partner);
+            }
+            if (turns && kind != 2) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], cs[e], __fmul_rn(p[e], sn[e]));
+            }
+        }
+        float scale = 1.f;
+        if constexpr (FMT == QWEN2_KV_INT8 || FMT == QWEN2_KV_E4M3) {
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(x[e]));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+            scale = m == 0.f ? 1.f : __fdiv_rn(m, FMT == QWEN2_KV_INT8 ? 127.f : 448.f);
+        }
+        if (!live) continue;
+        if (kind == 0) {
+            *reinterpret_cast<uint4*>(a.q_out.data + (long long)row * a.q_out.row_bytes +
+                                      (long long)h * a.q_out.head_bytes + 16 * c) = pack8_16(x, a.out_bf16);
+            continue;
+        }
+        char* dst = (kind == 1 ? a.kv.k : a.kv.v) + (long long)page * a.kv.page_bytes +
+                    (long long)off * a.kv.token_bytes + (long long)h * a.kv.head_bytes;
+        if constexpr (FMT == QWEN2_KV_F16 || FMT == QWEN2_KV_BF16) {
+            *reinterpret_cast<uint4*>(dst + 16 * c) = pack8_16(x, FMT == QWEN2_KV_BF16);
+        } else {
+            *reinterpret_cast<uint2*>(dst + 8 * c) = pack8_8<FMT>(x, scale);
+            if (c == 0)
+                (kind == 1 ? a.kv.k_scale : a.kv.v_scale)[(((long long)page * a.kv.n_kv + h) << a.kv.page_shift) + off] =
+                    scale;
+        }
+    }
+}
+
+struct ReadArgs {
+    Pool kv;
+    Batch b;
+    Rows k, v;
+    const int* out_start;
+    int n_out;
+};
+
+// Codes or 16-bit values as f32.
+template <int FMT, int N>
+__device__ __forceinline__ void widen(const uint4& raw, float (&x)[N]) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (FMT == QWEN2_KV_F16 || FMT == QWEN2_KV_BF16) {
+            float2 f;
+            if constexpr (FMT == QWEN2_KV_F16) f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        } else if constexpr (FMT == QWEN2_KV_INT8) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[4 * i + j] = (float)(int8_t)(w[i] >> (8 * j));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] >> (16 * j)), __NV_E4M3);
+                const float2 f = __half22float2(__half2(h));
+                x[4 * i + 2 * j] = f.x;
+                x[4 * i + 2 * j + 1] = f.y;
+            }
+        }
+    }
+}
+
+// A warp takes kReadRows consecutive output rows: lane l looks up row l (one
+// chain of dependent loads for all of them), then the warp streams their heads.
+constexpr int kReadRows = 4;
+
+template <int FMT, int DT, int HD>
+__global__ void __launch_bounds__(kRowThreads) k_paged_read(const __grid_constant__ ReadArgs a) {
+    constexpr bool k8 = FMT == QWEN2_KV_INT8 || FMT == QWEN2_KV_E4M3;
+    constexpr int kN = k8 ? 16 : 8;           // dims per lane
+    constexpr int kLanes = HD / kN;
+    constexpr int kHeads = 32 / kLanes;
+    constexpr int kOut = DT == QWEN2_DTYPE_F32 ? 4 : 2;
+    const int lane = threadIdx.x & 31;
+    const long long first = ((long long)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * kReadRows;
+    if (first >= a.n_out) return;
+    int page = -1, off = 0;
+    if (lane < kReadRows && first + lane < a.n_out) {
+        const int row = (int)first + lane;
+        int lo = 0, hi = a.b.n_seq;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldg(a.out_start + mid + 1) <= row) lo = mid + 1;
+            else hi = mid;
+        }
+        if (lo < a.b.n_seq) {
+            const int pos = row - __ldg(a.out_start + lo);
+            const int kv = __ldg(a.b.kv_len + lo);
+            const bool bad_len = kv < 0 || kv > ((long long)a.b.max_pages << a.kv.page_shift);
+            if (bad_len) raise_guard(a.b.guard, kGuardPosition);
+            else if (pos >= 0 && pos < kv) {
+                page = __ldg(a.b.pages + (long long)lo * a.b.pages_stride + (pos >> a.kv.page_shift));
+                off = pos & ((1 << a.kv.page_shift) - 1);
+                if ((unsigned)page >= (unsigned)a.kv.n_pages) {
+                    raise_guard(a.b.guard, QWEN2_GUARD_PAGE);
+                    page = -1;
+                }
+            }
+        }
+    }
+    const int c = lane % kLanes, sub = lane / kLanes;
+    const int n_slots = 2 * a.kv.n_kv;
+#pragma unroll
+    for (int r = 0; r < kReadRows; ++r) {
+        const int pg = __shfl_sync(0xffffffffu, page, r), of = __shfl_sync(0xffffffffu, off, r);
+        if (pg < 0) continue;
+        for (int slot = sub; slot < n_slots; slot += kHeads) {
+            const bool is_v = slot >= a.kv.n_kv;
+            const int h = is_v ? slot - a.kv.n_kv : slot;
+            const char* src = (is_v ? a.kv.v : a.kv.k) + (long long)pg * a.kv.page_bytes +
+                              (long long)of * a.kv.token_bytes + (long long)h * a.kv.head_bytes + 16 * c;
+            const uint4 raw = ld_stream_v4(src);
+            float x[kN];
+            widen<FMT, kN>(raw, x);
+            if constexpr (k8) {
+                const float s = __ldg((is_v ? a.kv.v_scale : a.kv.k_scale) +
+                                      (((long long)pg * a.kv.n_kv + h) << a.kv.page_shift) + of);
+#pragma unroll
+                for (int e = 0; e < kN; ++e) x[e] *= s;
+            }
+            const Rows& o = is_v ? a.v : a.k;
+            char* dst = o.data + (first + r) * o.row_bytes + (long long)h * o.head_bytes + (long long)kN * kOut * c;
+            if constexpr (DT == QWEN2_DTYPE_F32) {
+#pragma unroll
+                for (int e = 0; e < kN / 4; ++e)
+                    reinterpret_cast<float4*>(dst)[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kN / 8; ++e) {
+                    const float y[8] = {x[8 * e], x[8 * e + 1], x[8 * e + 2], x[8 * e + 3],
+                                        x[8 * e + 4], x[8 * e + 5], x[8 * e + 6], x[8 * e + 7]};
+                    reinterpret_cast<uint4*>(dst)[e] = pack8_16(y, DT == QWEN2_DTYPE_BF16);
+                }
+            }
+        }
+    }
+}
+
+template <int DT, int FMT>
+cudaError_t launch_write_hd(const WriteArgs& a, int head_dim, cudaStream_t st) {
+    const long long warps = (long long)a.b.n_rows * a.slices;
+    const unsigned blocks = (unsigned)((warps + kRowThreads / 32 - 1) / (kRowThreads / 32));
+    if (head_dim == 64) k_paged_write<DT, FMT, 64><<<blocks, kRowThreads, 0, st>>>(a);
+    else k_paged_write<DT, FMT, 128><<<blocks, kRowThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int DT>
+cudaError_t launch_write_fmt(const WriteArgs& a, int format, int head_dim, cudaStream_t st) {
+    switch (format) {
+        case QWEN2_KV_F16: return launch_write_hd<DT, QWEN2_KV_F16>(a, head_dim, st);
+        case QWEN2_KV_BF16: return launch_write_hd<DT, QWEN2_KV_BF16>(a, head_dim, st);
+        case QWEN2_KV_INT8: return launch_write_hd<DT, QWEN2_KV_INT8>(a, head_dim, st);
+        default: return launch_write_hd<DT, QWEN2_KV_E4M3>(a, head_dim, st);
+    }
+}
+
+template <int FMT, int DT>
+cudaError_t launch_read_hd(const ReadArgs& a, int head_dim, cudaStream_t st) {
+    const int per = kRowThreads / 32 * kReadRows;
+    const unsigned blocks = (unsigned)((a.n_out + (long long)per - 1) / per);
+    if (head_dim == 64) k_paged_read<FMT, DT, 64><<<blocks, kRowThreads, 0, st>>>(a);
+    else k_paged_read<FMT, DT, 128><<<blocks, kRowThreads, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <int FMT>
+cudaError_t launch_read_dt(const ReadArgs& a, int dtype, int head_dim, cudaStream_t st) {
+    switch (dtype) {
+        case QWEN2_DTYPE_F32: return launch_read_hd<FMT, QWEN2_DTYPE_F32>(a, head_dim, st);
+        case QWEN2_DTYPE_F16: return launch_read_hd<FMT, QWEN2_DTYPE_F16>(a, head_dim, st);
+        default: return launch_read_hd<FMT, QWEN2_DTYPE_BF16>(a, head_dim, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t enqueue_write(const Pool& kv, const Batch& b, const qwen2_paged_write_opts* o, int format, int head_dim,
+                          int n_head, int dtype, bool out_bf16, const Rows& q, const Rows& q_out, const Rows& k,
+                          const Rows& v, cudaStream_t st) {
+    WriteArgs a{};
+    a.kv = kv;
+    a.b = b;
+    a.q = q;
+    a.q_out = q_out;
+    a.k = k;
+    a.v = v;
+    a.n_head = n_head;
+    a.out_bf16 = out_bf16;
+    if (o) {
+        a.q_norm = n_head ? o->q_norm : nullptr;
+        a.k_norm = o->k_norm;
+        a.eps = o->norm_eps;
+        a.rope = o->rope;
+        a.rope_rows = o->rope_rows;
+        a.rotary = o->rope ? o->rotary_dim : 0;
+        a.interleaved = o->interleaved;
+    }
+    // One warp per step of heads while that leaves the device unfilled, so
+    // that a decode step's few rows are one round of loads; one warp per row
+    // once the rows alone fill it, so that a row's lookups are made once.
+    const int heads = head_dim == 64 ? 4 : 2;
+    const int steps = (n_head + 2 * kv.n_kv + heads - 1) / heads;
+    int per_warp = 1;
+    while (per_warp < steps && (long long)b.n_rows * steps / per_warp > 152 * 32) per_warp *= 2;
+    a.slices = (steps + per_warp - 1) / per_warp;
+    switch (dtype) {
+        case QWEN2_DTYPE_F32: return launch_write_fmt<QWEN2_DTYPE_F32>(a, format, head_dim, st);
+        case QWEN2_DTYPE_F16: return launch_write_fmt<QWEN2_DTYPE_F16>(a, format, head_dim, st);
+        default: return launch_write_fmt<QWEN2_DTYPE_BF16>(a, format, head_dim, st);
+    }
+}
+
+cudaError_t enqueue_read(const Pool& kv, const Batch& b, int format, int head_dim, const int* out_start, int n_out,
+                         int dtype, const Rows& k, const Rows& v, cudaStream_t st) {
+    ReadArgs a{kv, b, k, v, out_start, n_out};
+    switch (format) {
+        case QWEN2_KV_F16: return launch_read_dt<QWEN2_KV_F16>(a, dtype, head_dim, st);
+        case QWEN2_KV_BF16: return launch_read_dt<QWEN2_KV_BF16>(a, dtype, head_dim, st);
+        case QWEN2_KV_INT8: return launch_read_dt<QWEN2_KV_INT8>(a, dtype, head_dim, st);
+        default: return launch_read_dt<QWEN2_KV_E4M3>(a, dtype, head_dim, st);
+    }
+}
+
+}  // namespace paged
+}  // namespace qwen2

@@ -1,0 +1,357 @@
+"""Paged key / value cache: the pool and batch descriptors and the operators
+over them (``qwen2_paged_*`` of ``include/qwen2.h``).
+
+    pool = q2.PagedKV.zeros(n_pages, 64, n_kv_head, head_dim, q2.KV_INT8)
+    batch = q2.PagedBatch(q_start, kv_len, pages, max_q)     # int32 CUDA tensors
+    q = q2.paged_write(pool, batch, k, v, q=q, q_dtype=torch.bfloat16, rope=table)
+    o = q2.paged_attention(pool, batch, q)
+
+Argument marshalling only; every check that needs a value in device memory is
+the kernels' own and is reported through ``PagedBatch.check``.  Calls do not
+synchronise and may be captured into a CUDA graph: a replay reads the batch's
+tensors anew.  Outputs and workspaces come from torch's allocator on the
+stream of the call.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+
+KV_F16 = 0
+KV_BF16 = 1
+KV_INT8 = 2
+KV_E4M3 = 3
+
+ROPE_PLAIN = 0
+ROPE_LINEAR = 1
+ROPE_YARN = 2
+
+_P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", _P), ("dtype", _I32), ("row_stride", _I64), ("head_stride", _I64)]
+
+
+class _PagedKV(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("format", _I32), ("n_pages", _I32),
+                ("page_size", _I32), ("n_kv_head", _I32), ("head_dim", _I32), ("page_stride", _I64),
+                ("token_stride", _I64), ("head_stride", _I64)]
+
+
+class _PagedBatch(ctypes.Structure):
+    _fields_ = [("n_seq", _I32), ("n_rows", _I32), ("max_q", _I32), ("max_pages", _I32), ("pages_stride", _I64),
+                ("q_start", _P), ("kv_len", _P), ("pages", _P), ("guard", _P)]
+
+
+class _WriteOpts(ctypes.Structure):
+    _fields_ = [("q_norm", _P), ("k_norm", _P), ("norm_eps", ctypes.c_float), ("rope", _P), ("rope_rows", _I32),
+                ("rotary_dim", _I32), ("interleaved", _I32)]
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", _I32), ("factor", ctypes.c_double), ("original_rows", _I32),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double)]
+
+
+_bound = None
+
+
+def _lib():
+    global _bound
+    if _bound is None:
+        from . import lib
+        L = lib()
+        L.qwen2_rope_table.argtypes = [_I32, _I32, ctypes.c_double, _P, _P]
+        L.qwen2_paged_write.argtypes = [_P, _P, _P, _I32, _P, _P, _P, _P, _P]
+        L.qwen2_paged_read.argtypes = [_P, _P, _P, _I32, _P, _P, _P]
+        L.qwen2_paged_attention.argtypes = [_P, _P, _I32, _P, _P, _P, ctypes.c_float, _I32, _P, _I64, _P]
+        for f in (L.qwen2_rope_table, L.qwen2_paged_write, L.qwen2_paged_read, L.qwen2_paged_attention):
+            f.restype = ctypes.c_int
+        L.qwen2_paged_attention_workspace.argtypes = [_P, _P, _I32]
+        L.qwen2_paged_attention_workspace.restype = _I64
+        _bound = L
+    return _bound
+
+
+def _check(rc: int):
+    if rc:
+        from . import Qwen2Error
+        raise Qwen2Error(rc, _lib().qwen2_last_error(None).decode())
+
+
+_dtypes = {}     # torch dtype -> QWEN2_DTYPE_*
+_formats = {}    # torch dtype -> QWEN2_KV_*
+
+
+def _types():
+    if not _dtypes:
+        import torch
+        _formats.update({torch.float16: KV_F16, torch.bfloat16: KV_BF16, torch.int8: KV_INT8,
+                         torch.float8_e4m3fn: KV_E4M3})
+        _dtypes.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    return _dtypes
+
+
+def rope_table(rows: int, rotary_dim: int, theta: float = 1e6, kind: int = ROPE_PLAIN, factor: float = 1.0,
+               original_rows: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0) -> np.ndarray:
+    """(cos, sin) of position * theta^(-2i / rotary_dim), computed in double:
+    f32 [rows, rotary_dim / 2, 2], host memory.  ``kind`` ROPE_LINEAR divides
+    every angle by ``factor``; ROPE_YARN divides the slow dims' angles and
+    scales the table (``original_rows``: the context trained at)."""
+    out = np.empty((max(int(rows), 0), max(int(rotary_dim), 0) // 2, 2), dtype=np.float32)
+    s = _RopeScaling(kind, factor, original_rows, beta_fast, beta_slow)
+    _check(_lib().qwen2_rope_table(rows, rotary_dim, theta, ctypes.addressof(s), out.ctypes.data))
+    return out
+
+
+class PagedKV:
+    """A pool of pages.  ``k``, ``v``: [n_pages, page_size, n_kv_head, head_dim]
+    CUDA tensors (f16, bf16, int8 or float8_e4m3fn) of equal strides, the last
+    dim contiguous; head-major pages are a permuted view.  ``k_scale``,
+    ``v_scale`` (8-bit pools): f32 [n_pages, n_kv_head, page_size], contiguous."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        _types()
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must be [n_pages, page_size, n_kv_head, head_dim]")
+        if k.dtype not in _formats or v.dtype != k.dtype:
+            raise ValueError(f"pages of {k.dtype} / {v.dtype} are not supported")
+        if not (k.is_cuda and v.device == k.device):
+            raise ValueError("k and v must be on one CUDA device")
+        if v.stride() != k.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must have the same strides and contiguous heads")
+        self.format = _formats[k.dtype]
+        if self.format in (KV_INT8, KV_E4M3):
+            want = (k.shape[0], k.shape[2], k.shape[1])
+            for s in (k_scale, v_scale):
+                if s is None or tuple(s.shape) != want or str(s.dtype) != "torch.float32" or \
+                        s.device != k.device or not s.is_contiguous():
+                    raise ValueError("8-bit pages need contiguous f32 scales [n_pages, n_kv_head, page_size]")
+        else:
+            k_scale = v_scale = None
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device = k.device
+        self.n_pages, self.page_size, self.n_kv_head, self.head_dim = k.shape
+        self._c = _PagedKV(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
+                           v_scale.data_ptr() if v_scale is not None else None, self.format, self.n_pages,
+                           self.page_size, self.n_kv_head, self.head_dim, *k.stride()[:3])
+        self._at = ctypes.addressof(self._c)
+        self._shape = (self.n_kv_head, self.head_dim)
+
+    @classmethod
+    def zeros(cls, n_pages: int, page_size: int, n_kv_head: int, head_dim: int, format: int, device="cuda"):
+        """A pool of zeroed, head-major pages."""
+        import torch
+        _types()
+        dtype = next(d for d, f in _formats.items() if f == format)
+        k, v = (torch.zeros((n_pages, n_kv_head, page_size, head_dim), dtype=torch.int8 if dtype.itemsize == 1 else dtype,
+                            device=device).view(dtype).permute(0, 2, 1, 3) for _ in range(2))
+        ks = vs = None
+        if dtype.itemsize == 1:
+            ks, vs = (torch.ones((n_pages, n_kv_head, page_size), dtype=torch.float32, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+
+class PagedBatch:
+    """The new rows of a batch and its pages, int32 CUDA tensors: ``q_start``
+    [n_seq + 1] (row r of sequence s: q_start[s] <= r < q_start[s + 1]),
+    ``kv_len`` [n_seq] (positions in the cache, the new rows included) and
+    ``pages`` [n_seq, max_pages].  ``max_q``: an upper bound on the rows of one
+    sequence.  The tensors are read by every call (and every graph replay)
+    anew and may be changed in place between them."""
+
+    def __init__(self, q_start, kv_len, pages, max_q: int):
+        import torch
+        _types()
+        n = kv_len.shape[0] if kv_len.dim() == 1 else -1
+        if n < 1 or tuple(q_start.shape) != (n + 1,) or pages.dim() != 2 or pages.shape[0] != n or pages.shape[1] < 1:
+            raise ValueError("q_start must be [n_seq + 1], kv_len [n_seq] and pages [n_seq, max_pages]")
+        for t in (q_start, kv_len, pages):
+            if t.dtype != torch.int32 or not t.is_cuda or t.device != kv_len.device or t.stride(-1) != 1:
+                raise ValueError("q_start, kv_len and pages must be int32 CUDA tensors, contiguous in their last dim")
+        if n > 1 and pages.stride(0) < pages.shape[1]:
+            raise ValueError("the rows of pages overlap")
+        self.q_start, self.kv_len, self.pages = q_start, kv_len, pages
+        self.device = kv_len.device
+        self.n_seq, self.max_q = n, int(max_q)
+        self.guard = torch.zeros(1, dtype=torch.int32, device=self.device)
+        stride = max(pages.stride(0), pages.shape[1])
+        self._c = _PagedBatch(n, 0, self.max_q, pages.shape[1], stride, q_start.data_ptr(), kv_len.data_ptr(),
+                              pages.data_ptr(), self.guard.data_ptr())
+        self._at = ctypes.addressof(self._c)
+        self._space = {}
+
+    def check(self):
+        """Synchronises, and raises Qwen2Error (QWEN2_E_DEVICE_GUARD) if a
+        value in the batch's tensors was bad in any call since the last check."""
+        from . import QWEN2_E_DEVICE_GUARD, Qwen2Error
+        code = int(self.guard.item())
+        if code:
+            self.guard.zero_()
+            names = {1: "position outside the pages or the rotation table", 3: "bad q_start", 4: "bounded wait timed out",
+                     5: "page id outside the pool"}
+            raise Qwen2Error(QWEN2_E_DEVICE_GUARD, f"device guard {code}: {names.get(code, 'unknown')}")
+
+
+def _rows(t, name: str, shape, device):
+    """The descriptor of a [rows, heads, head_dim] tensor; shape: (heads or None, head_dim)."""
+    if t.dim() != 3 or t.shape[2] != shape[1] or (shape[0] is not None and t.shape[1] != shape[0]):
+        raise ValueError(f"{name} must be [rows, {shape[0] if shape[0] is not None else 'heads'}, {shape[1]}]")
+    dt = _dtypes.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name}: {t.dtype} is not supported")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    rs, hs, es = t.stride()
+    if es != 1:
+        raise ValueError(f"{name}: heads must be contiguous")
+    return _Rows(t.data_ptr(), dt, rs, hs)
+
+
+def _on_stream(kv, batch, stream, call):
+    """Runs ``call(stream pointer)`` with the pool's device current and, where
+    the caller names a stream, with that stream current, so that outputs and
+    workspaces are allocated for it."""
+    import torch
+    if batch.device != kv.device:
+        raise ValueError("the pool and the batch are on different devices")
+    if stream is not None:
+        if stream.device != kv.device:
+            raise ValueError("the stream belongs to another device")
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    if torch.cuda.current_device() != kv.device.index:
+        with torch.cuda.device(kv.device):
+            return call(torch.cuda.current_stream().cuda_stream)
+    return call(torch.cuda.current_stream().cuda_stream)
+
+
+def _f32(t, name: str, shape, device):
+    if str(t.dtype) != "torch.float32" or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous f32 tensor of shape {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def paged_write(kv: PagedKV, batch: PagedBatch, k, v, q=None, q_out=None, q_dtype=None, q_norm=None, k_norm=None,
+                norm_eps: float = 1e-6, rope=None, interleaved: bool = False, stream=None):
+    """Store the batch's ``k``, ``v`` rows ([rows, n_kv_head, head_dim], f32 /
+    f16 / bf16) in their pages, and return the finished queries of ``q``
+    ([rows, n_head, head_dim]; None without).  ``q_norm`` / ``k_norm`` (f32
+    [head_dim]): RMSNorm of every head; ``rope`` (f32 [positions, rotary_dim /
+    2, 2], see rope_table): rotation of the leading rotary_dim dims of q and k
+    at each row's position, dims paired (i, i + rotary_dim / 2) or, if
+    ``interleaved``, (2i, 2i + 1).  Queries come in ``q_dtype`` (default: the
+    pages' type if 16-bit, else q's if 16-bit, else f16)."""
+    def call(st):
+        import torch
+        rows = k.shape[0]
+        rk, rv = _rows(k, "k", kv._shape, kv.device), _rows(v, "v", kv._shape, kv.device)
+        if v.shape[0] != rows:
+            raise ValueError("k and v must have the same rows")
+        out, n_head, rq, ro = None, 0, None, None
+        if q is not None:
+            if q.shape[0] != rows:
+                raise ValueError("q and k must have the same rows")
+            rq = _rows(q, "q", (None, kv.head_dim), kv.device)
+            n_head = q.shape[1]
+            out = q_out
+            if out is None:
+                dt = q_dtype or (kv.k.dtype if kv.format <= KV_BF16 else
+                                 q.dtype if q.dtype != torch.float32 else torch.float16)
+                out = torch.empty((rows, n_head, kv.head_dim), dtype=dt, device=kv.device)
+            ro = _rows(out, "q_out", (n_head, kv.head_dim), kv.device)
+            if out.shape[0] != rows:
+                raise ValueError("q_out and q must have the same rows")
+        elif q_out is not None or q_norm is not None:
+            raise ValueError("q_out and q_norm need q")
+        o = _WriteOpts(norm_eps=norm_eps)
+        if q_norm is not None:
+            o.q_norm = _f32(q_norm, "q_norm", (kv.head_dim,), kv.device)
+        if k_norm is not None:
+            o.k_norm = _f32(k_norm, "k_norm", (kv.head_dim,), kv.device)
+        if rope is not None:
+            if rope.dim() != 3 or rope.shape[2] != 2:
+                raise ValueError("rope must be [positions, rotary_dim / 2, 2]")
+            o.rope = _f32(rope, "rope", tuple(rope.shape), kv.device)
+            o.rope_rows, o.rotary_dim, o.interleaved = rope.shape[0], 2 * rope.shape[1], int(interleaved)
+        batch._c.n_rows = rows
+        _check(_lib().qwen2_paged_write(kv._at, batch._at, ctypes.addressof(o), n_head,
+                                        ctypes.addressof(rq) if rq else None, ctypes.addressof(ro) if ro else None,
+                                        ctypes.addressof(rk), ctypes.addressof(rv), st))
+        return out
+    return _on_stream(kv, batch, stream, call)
+
+
+def paged_read(kv: PagedKV, batch: PagedBatch, out_start, n_rows: int, dtype=None, k_out=None, v_out=None, stream=None):
+    """Read the sequences' positions back as rows: position p of sequence s is
+    row out_start[s] + p of (k, v), [n_rows, n_kv_head, head_dim] in ``dtype``
+    (f32, f16 or bf16; default f32).  ``out_start``: int32 CUDA tensor
+    [n_seq + 1]; rows outside the sequences are left as they were."""
+    def call(st):
+        import torch
+        if tuple(out_start.shape) != (batch.n_seq + 1,) or out_start.dtype != torch.int32 or \
+                out_start.device != kv.device or not out_start.is_contiguous():
+            raise ValueError("out_start must be a contiguous int32 tensor [n_seq + 1] on the pool's device")
+        if (k_out is None) != (v_out is None):
+            raise ValueError("k_out and v_out go together")
+        ko, vo = k_out, v_out
+        if ko is None:
+            shape = (n_rows, *kv._shape)
+            ko = torch.empty(shape, dtype=dtype or torch.float32, device=kv.device)
+            vo = torch.empty(shape, dtype=dtype or torch.float32, device=kv.device)
+        rk, rv = _rows(ko, "k_out", kv._shape, kv.device), _rows(vo, "v_out", kv._shape, kv.device)
+        if ko.shape[0] < n_rows or vo.shape[0] < n_rows:
+            raise ValueError("k_out and v_out need n_rows rows")
+        _check(_lib().qwen2_paged_read(kv._at, batch._at, out_start.data_ptr(), n_rows, ctypes.addressof(rk),
+                                       ctypes.addressof(rv), st))
+        return ko, vo
+    return _on_stream(kv, batch, stream, call)
+
+
+def paged_attention(kv: PagedKV, batch: PagedBatch, q, out=None, scale=None, causal: bool = True,
+                    return_lse: bool = False, workspace=None, stream=None):
+    """Attention of the batch's rows ``q`` ([rows, n_head, head_dim], f16 or
+    bf16, the pages' type where they are 16-bit) over its pages; row i of a
+    sequence with n rows sees positions <= kv_len - n + i (``causal``) or all
+    of them.  Returns o like q, with ``return_lse`` also f32 [rows, n_head]:
+    the log of the sum of exp(scale q.k), -inf for a row without keys (whose o
+    is 0).  ``scale``: default head_dim^-1/2.  ``workspace``: a uint8 CUDA
+    tensor of ``paged_attention_workspace`` bytes (default: allocated here)."""
+    def call(st):
+        import torch
+        rows, n_head = q.shape[0], q.shape[1]
+        rq = _rows(q, "q", (None, kv.head_dim), kv.device)
+        o = torch.empty(q.shape, dtype=q.dtype, device=kv.device) if out is None else out
+        ro = _rows(o, "out", (n_head, kv.head_dim), kv.device)
+        if o.shape[0] != rows:
+            raise ValueError("out and q must have the same rows")
+        lse = torch.empty((rows, n_head), dtype=torch.float32, device=kv.device) if return_lse else None
+        batch._c.n_rows = rows
+        ws = workspace
+        if ws is None:
+            key = (kv._shape, n_head)
+            need = batch._space.get(key)
+            if need is None:
+                need = batch._space[key] = paged_attention_workspace(kv, batch, n_head)
+            ws = torch.empty(need, dtype=torch.uint8, device=kv.device)
+        elif ws.dtype != torch.uint8 or ws.device != kv.device or not ws.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor on the pool's device")
+        _check(_lib().qwen2_paged_attention(kv._at, batch._at, n_head, ctypes.addressof(rq), ctypes.addressof(ro),
+                                            lse.data_ptr() if return_lse else None,
+                                            kv.head_dim ** -0.5 if scale is None else scale, int(causal),
+                                            ws.data_ptr(), ws.numel(), st))
+        return (o, lse) if return_lse else o
+    return _on_stream(kv, batch, stream, call)
+
+
+def paged_attention_workspace(kv: PagedKV, batch: PagedBatch, n_head: int) -> int:
+    """Workspace bytes of paged_attention for these shapes."""
+    import torch
+    with torch.cuda.device(kv.device):
+        need = _lib().qwen2_paged_attention_workspace(kv._at, batch._at, n_head)
+    if need < 0:
+        from . import QWEN2_E_ARG, Qwen2Error
+        raise Qwen2Error(QWEN2_E_ARG, _lib().qwen2_last_error(None).decode())
+    return need
