@@ -315,7 +315,7 @@ def test_graph_replays_read_lengths_and_pages_anew(q2):
     with torch.cuda.graph(graph):
         out = step()
     spare = [i for i in range(c.kv.n_pages) if not (c.pages == i).any()]
-    for lens in ([200, 77, 31], [199, 78, 32], [150, 80, 33], [3, 1, 17]):
+    for lens in ([200, 77, 31], [199, 78, 32], [150, 79, 33], [3, 1, 17]):
         x.copy_(c.normal(3, 18, 64))
         c.batch.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
         if lens[2] == 33:
