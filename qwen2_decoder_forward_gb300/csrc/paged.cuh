@@ -54,7 +54,7 @@ __device__ __forceinline__ Seq load_seq(const Batch& b, int page_shift, int s) {
 // ---- the attention kernels' work list -------------------------------------------
 // The query rows of one sequence and kv head are the pairs (row, query head of
 // the group), row-major: packed row i = row * group + head.  They are cut into
-// tiles of kRows packed rows, and each tile's keys into units of kKeys
+// tiles of `tile` packed rows, and each tile's keys into units of kKeys
 // positions; a tile without keys is one unit.  The units of all tiles, ordered
 // (sequence, kv head, tile, unit), form one list, of which CTA c of g takes
 // the contiguous part [W c / g, W (c + 1) / g): every CTA has the same work
@@ -69,14 +69,10 @@ __device__ __forceinline__ int tile_keys(const Seq& q, int group, int i0, int ro
     const int last = (min(i0 + rows, q.n * group) - 1) / group;
     return max(0, q.kv - q.n + last + 1);
 }
-// Units of one kv head of a sequence, over its tiles.
-__device__ __forceinline__ long long head_units(const Seq& q, int group, int rows, int keys, bool causal) {
-    const int packed = q.n * group;
-    const int tiles = (packed + rows - 1) / rows;
-    if (!causal) return (long long)tiles * max(1, (q.kv + keys - 1) / keys);
-    long long u = 0;
-    for (int t = 0; t < tiles; ++t) u += max(1, (tile_keys(q, group, t * rows, rows, true) + keys - 1) / keys);
-    return u;
+// Units of one tile.
+template <int kKeys>
+__device__ __forceinline__ int tile_units(const Seq& q, int group, int t, int rows, bool causal) {
+    return max(1, (tile_keys(q, group, t * rows, rows, causal) + kKeys - 1) / kKeys);
 }
 
 // What a CTA left in the workspace: slot 0 the part of a tile that an earlier
@@ -119,6 +115,7 @@ struct AttnArgs {
     int causal;
     float scale_log2;        // scale * log2(e): the softmax runs in base 2
     int rows_lo, rows_hi;    // this kernel's sequences: rows_lo < packed rows <= rows_hi
+    int tile;                // packed rows per tile
     Parts parts;
 };
 
@@ -145,13 +142,34 @@ __device__ __forceinline__ bool owns(const AttnArgs& a, const Seq& q) {
 // Builds the prefix sums with the whole block (at most 4096 sequences) and
 // returns this CTA's share.  min_units: a CTA gets at least that many units
 // (but the last), so that small batches are not cut finer than pays.
-template <int kRows, int kKeys>
+template <int kKeys>
 __device__ __forceinline__ WorkList build_work(const AttnArgs& a, long long* prefix, int min_units) {
+    // A thread per sequence; one with many causal tiles (each of its own length)
+    // is left to a whole warp.
     for (int s = threadIdx.x; s < a.b.n_seq; s += blockDim.x) {
         const Seq q = load_seq(a.b, a.kv.page_shift, s);
         if (blockIdx.x == 0 && (q.bad_rows || q.bad_len))
             raise_guard(a.b.guard, q.bad_rows ? kGuardShape : kGuardPosition);
-        prefix[s + 1] = owns(a, q) ? head_units(q, a.group, kRows, kKeys, a.causal) * a.kv.n_kv : 0;
+        long long u = 0;
+        if (owns(a, q)) {
+            const int tiles = (q.n * a.group + a.tile - 1) / a.tile;
+            if (!a.causal) u = (long long)tiles * tile_units<kKeys>(q, a.group, 0, a.tile, false);
+            else if (tiles <= 4)
+                for (int t = 0; t < tiles; ++t) u += tile_units<kKeys>(q, a.group, t, a.tile, true);
+            else u = -1;
+        }
+        prefix[s + 1] = u < 0 ? u : u * a.kv.n_kv;
+    }
+    __syncthreads();
+    for (int s = threadIdx.x >> 5; s < a.b.n_seq; s += blockDim.x >> 5) {
+        if (prefix[s + 1] >= 0) continue;
+        const Seq q = load_seq(a.b, a.kv.page_shift, s);
+        const int tiles = (q.n * a.group + a.tile - 1) / a.tile;
+        long long u = 0;
+        for (int t = threadIdx.x & 31; t < tiles; t += 32) u += tile_units<kKeys>(q, a.group, t, a.tile, true);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+        if ((threadIdx.x & 31) == 0) prefix[s + 1] = u * a.kv.n_kv;
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -185,7 +203,8 @@ __device__ __forceinline__ WorkList build_work(const AttnArgs& a, long long* pre
 }
 
 // The tile that holds unit `u` of the list, with up to `left` units of it.
-template <int kRows, int kKeys>
+// Called by whole warps.
+template <int kKeys>
 __device__ __forceinline__ Tile find_tile(const AttnArgs& a, const WorkList& w, long long u, long long left) {
     int lo = 0, hi = a.b.n_seq;          // largest s with prefix[s] <= u and units of its own
     while (hi - lo > 1) {
@@ -200,29 +219,46 @@ __device__ __forceinline__ Tile find_tile(const AttnArgs& a, const WorkList& w, 
     long long r = u - w.prefix[lo];
     t.head = (int)(r / per_head);
     r -= t.head * per_head;
+    const int tiles = (t.q.n * a.group + a.tile - 1) / a.tile;
     if (!a.causal) {
-        t.keys = t.q.kv;
-        t.units = max(1, (t.keys + kKeys - 1) / kKeys);
+        t.units = tile_units<kKeys>(t.q, a.group, 0, a.tile, false);
         t.t = (int)(r / t.units);
         r -= (long long)t.t * t.units;
     } else {
-        const int tiles = (t.q.n * a.group + kRows - 1) / kRows;
-        for (t.t = 0;; ++t.t) {
-            t.keys = tile_keys(t.q, a.group, t.t * kRows, kRows, true);
-            t.units = max(1, (t.keys + kKeys - 1) / kKeys);
-            if (r < t.units || t.t + 1 >= tiles) break;
-            r -= t.units;
+        // 32 tiles at a time: the first one whose units reach past r.
+        const int lane = threadIdx.x & 31;
+        for (int t0 = 0;; t0 += 32) {
+            const int own = t0 + lane < tiles ? tile_units<kKeys>(t.q, a.group, t0 + lane, a.tile, true) : 0;
+            long long sum = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += x;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, sum > r);
+            const int at = hit ? __ffs(hit) - 1 : 31;
+            const long long before = __shfl_sync(0xffffffffu, sum - own, at);
+            t.units = __shfl_sync(0xffffffffu, own, at);
+            t.t = t0 + at;
+            if (hit || t0 + 32 >= tiles) {
+                r -= before;
+                break;
+            }
+            r -= __shfl_sync(0xffffffffu, sum, 31);
         }
+        t.t = min(t.t, tiles - 1);
     }
+    t.keys = tile_keys(t.q, a.group, t.t * a.tile, a.tile, a.causal);
+    t.units = max(1, t.units);
     t.u0 = (int)r;
     t.n = max(1, (int)min((long long)(t.units - t.u0), left));
     return t;
 }
 
 // The tile after `t` in the list.
-template <int kRows, int kKeys>
+template <int kKeys>
 __device__ __forceinline__ void next_tile(const AttnArgs& a, const WorkList& w, Tile& t, long long left) {
-    const int tiles = (t.q.n * a.group + kRows - 1) / kRows;
+    const int tiles = (t.q.n * a.group + a.tile - 1) / a.tile;
     if (++t.t == tiles) {
         t.t = 0;
         if (++t.head == a.kv.n_kv) {
@@ -233,7 +269,7 @@ __device__ __forceinline__ void next_tile(const AttnArgs& a, const WorkList& w, 
             t.q = load_seq(a.b, a.kv.page_shift, t.s);
         }
     }
-    t.keys = tile_keys(t.q, a.group, t.t * kRows, kRows, a.causal);
+    t.keys = tile_keys(t.q, a.group, t.t * a.tile, a.tile, a.causal);
     t.units = max(1, (t.keys + kKeys - 1) / kKeys);
     t.u0 = 0;
     t.n = (int)min((long long)t.units, left);

@@ -181,13 +181,13 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t4 = lane & 3;
-    const WorkList work = build_work<kRows, kUnit>(a, prefix, 1);
+    const WorkList work = build_work<kUnit>(a, prefix, 1);
     const int slot0 = 2 * blockIdx.x;
     bool wrote0 = false, wrote1 = false;
     long long left = work.end - work.begin;
     if (left > 0) {
         const uint32_t ring = (uint32_t)__cvta_generic_to_shared(rings + warp * S::kRing);
-        Tile t = find_tile<kRows, kUnit>(a, work, work.begin, left);
+        Tile t = find_tile<kUnit>(a, work, work.begin, left);
         Feed f{t, 0, left};
         int f_page = -1;
         // Page of the feed's current step; -1 if it has no keys, -2 if its id is bad.
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
                 --f.left;
                 if (++f.i == f.t.n) {
                     f.i = 0;
-                    if (f.left > 0) next_tile<kRows, kUnit>(a, work, f.t, f.left);
+                    if (f.left > 0) next_tile<kUnit>(a, work, f.t, f.left);
                 }
             }
             f_page = look_up();
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
             __syncthreads();
             left -= t.n;
             if (left <= 0) break;
-            next_tile<kRows, kUnit>(a, work, t, left);
+            next_tile<kUnit>(a, work, t, left);
         }
         cp_wait<0>();
     }
@@ -589,25 +589,38 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
     if (!wrote1) store_part_none(a.parts, slot0 + 1);
 }
 
-// Adds up the tile that begins in CTA blockIdx.x's slot 1 and goes on in the
-// slots 0 of the CTAs after it: rows blockIdx.y, blockIdx.y + gridDim.y, ...
-// of it, a block per row, its warps taking the parts in turn.
+// What the join takes: the partials of the few-rows kernel's CTAs and of the
+// tensor-core kernel's (either may be absent).
+struct JoinArgs {
+    Rows out;
+    float* lse;
+    int n_head, group;
+    Parts parts[2];
+    int n_cta[2];
+};
+
+// Adds up the tile that begins in a CTA's slot 1 and goes on in the slots 0 of
+// the CTAs after it: rows blockIdx.y, blockIdx.y + gridDim.y, ... of it, a
+// block per row, its warps taking the parts in turn.  blockIdx.x counts the
+// CTAs of the first kernel, then those of the second.
 template <int HD, bool BF16>
-__global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ AttnArgs a, int n_cta) {
+__global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ JoinArgs a) {
     constexpr int kV = HD / 32;     // dims per lane
     __shared__ float so[4][HD], sl[4];
     pdl_launch_dependents();
     pdl_wait();
-    const int c0 = blockIdx.x;
-    const PartInfo first = a.parts.info[2 * c0 + 1];
+    const int which = (int)blockIdx.x >= a.n_cta[0];
+    const int c0 = blockIdx.x - (which ? a.n_cta[0] : 0), n_cta = a.n_cta[which];
+    const Parts& parts = a.parts[which];
+    const PartInfo first = parts.info[2 * c0 + 1];
     if (first.state == kPartNone) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rows = a.parts.rows;
+    const int rows = parts.rows;
     // Parts: slot 2 c0 + 1, then slots 2 c of the following CTAs up to the last.
     int n = 1;
     for (int c = c0 + 1;; ++n, ++c) {
         if (c >= n_cta) break;
-        const int st = a.parts.info[2 * c].state;
+        const int st = parts.info[2 * c].state;
         if (st == kPartNone) break;
         if (st & kPartLast) {
             ++n;
@@ -617,7 +630,7 @@ __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ AttnA
     for (int r = blockIdx.y; first.packed0 + r < first.packed_end; r += gridDim.y) {
         const auto slot = [&](int k) { return k == 0 ? 2 * c0 + 1 : 2 * (c0 + k); };
         float top = -INFINITY;
-        for (int k = lane; k < n; k += 32) top = fmaxf(top, a.parts.ml[(long long)slot(k) * 2 * rows + r]);
+        for (int k = lane; k < n; k += 32) top = fmaxf(top, parts.ml[(long long)slot(k) * 2 * rows + r]);
         top = warp_max(top);
         const float base = top == -INFINITY ? 0.f : top;
         float acc[kV], sum = 0.f;
@@ -625,10 +638,10 @@ __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ AttnA
         for (int e = 0; e < kV; ++e) acc[e] = 0.f;
 #pragma unroll 4
         for (int k = warp; k < n; k += 4) {
-            const float* ml = a.parts.ml + (long long)slot(k) * 2 * rows + r;
+            const float* ml = parts.ml + (long long)slot(k) * 2 * rows + r;
             const float w = ex2(ml[0] - base);
             sum = fmaf(ml[rows], w, sum);
-            const float* o = a.parts.o + ((long long)slot(k) * rows + r) * HD + kV * lane;
+            const float* o = parts.o + ((long long)slot(k) * rows + r) * HD + kV * lane;
 #pragma unroll
             for (int e = 0; e < kV; ++e) acc[e] = fmaf(o[e], w, acc[e]);
         }
@@ -658,38 +671,59 @@ __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ AttnA
 constexpr int kMaxCtasPerSm = 3;
 
 template <int HD, Kind K, bool BF16, int MT>
-cudaError_t launch_few(AttnArgs a, int n_sm, cudaStream_t st) {
+cudaError_t launch_few(AttnArgs& a, int* grid, int n_sm, cudaStream_t st) {
     using S = Shape<HD, K>;
     const size_t smem = (sizeof(Meet<HD, MT>) + 127) / 128 * 128 + kWarps * S::kRing + 8 * ((size_t)a.b.n_seq + 1);
     auto kern = k_paged_attn<HD, K, BF16, MT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     const int by_smem = (int)(228 * 1024 / (smem + 1024));
-    const int grid = n_sm * max(1, min(by_smem, MT == 1 ? kMaxCtasPerSm : 2));
-    a.parts = carve_parts(a.parts.info, grid, 16 * MT);
-    kern<<<grid, kThreads, smem, st>>>(a);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    return launch_pdl(k_attn_join<HD, BF16>, dim3(grid, 16), dim3(128), 0, st, a, grid);
+    *grid = n_sm * max(1, min(by_smem, MT == 1 ? kMaxCtasPerSm : 2));
+    a.parts = carve_parts(a.parts.info, *grid, 16 * MT);
+    kern<<<*grid, kThreads, smem, st>>>(a);
+    return cudaGetLastError();
 }
 
 template <int HD, Kind K, bool BF16>
-cudaError_t launch_rows(const AttnArgs& a, int mt, int n_sm, cudaStream_t st) {
-    return mt == 1 ? launch_few<HD, K, BF16, 1>(a, n_sm, st) : launch_few<HD, K, BF16, 2>(a, n_sm, st);
+cudaError_t launch_rows(AttnArgs& a, int* grid, int n_sm, cudaStream_t st) {
+    return a.tile == 16 ? launch_few<HD, K, BF16, 1>(a, grid, n_sm, st) : launch_few<HD, K, BF16, 2>(a, grid, n_sm, st);
 }
 
 template <int HD, bool BF16>
-cudaError_t launch_kind(const AttnArgs& a, int format, int mt, int n_sm, cudaStream_t st) {
-    if (format == QWEN2_KV_INT8) return launch_rows<HD, kInt8, BF16>(a, mt, n_sm, st);
-    if (format == QWEN2_KV_E4M3) return launch_rows<HD, kE4m3, BF16>(a, mt, n_sm, st);
-    return launch_rows<HD, kSame16, BF16>(a, mt, n_sm, st);
+cudaError_t launch_kind(AttnArgs& a, int format, int* grid, int n_sm, cudaStream_t st) {
+    if (format == QWEN2_KV_INT8) return launch_rows<HD, kInt8, BF16>(a, grid, n_sm, st);
+    if (format == QWEN2_KV_E4M3) return launch_rows<HD, kE4m3, BF16>(a, grid, n_sm, st);
+    return launch_rows<HD, kSame16, BF16>(a, grid, n_sm, st);
+}
+
+// Which kernels a call needs.  Sequences of up to 32 packed rows are the
+// few-rows kernel's, longer ones the tensor-core kernel's; where a batch may
+// have both, the few-rows kernel keeps to 16 rows.
+struct Plan {
+    int tile;            // packed rows of the few-rows kernel's tiles; 0: not launched
+    int few;             // most packed rows of its sequences
+    bool tc;
+};
+Plan plan_of(const Batch& b, const Pool& kv, int n_head, bool tensor) {
+    const int group = n_head / kv.n_kv;
+    const long long most = (long long)b.max_q * group;
+    if (most <= 16) return {16, 0x7fffffff, false};
+    if (most <= 32 || !tensor) return {32, 0x7fffffff, false};
+    if (b.n_seq == 1) return {0, 0, true};
+    return {16, 16, true};
+}
+bool tensor_kernel(const Pool& kv, int n_head, int format, float scale) {
+    // Masked scores are -inf before the scale: it has to be positive there.
+    return (format == QWEN2_KV_F16 || format == QWEN2_KV_BF16) && scale > 0.f && n_head / kv.n_kv <= 128;
 }
 
 }  // namespace
 
 long long attn_workspace(const Batch& b, const Pool& kv, int head_dim, int n_head, int n_sm) {
     const int group = n_head / kv.n_kv;
-    return parts_bytes(n_sm * kMaxCtasPerSm, (long long)b.max_q * group <= 16 ? 16 : 32, head_dim);
+    // For either choice of kernels.
+    return parts_bytes(n_sm * kMaxCtasPerSm, (long long)b.max_q * group <= 16 ? 16 : 32, head_dim) +
+           ((long long)b.max_q * group > 32 ? parts_bytes(n_sm, tc_tile_rows(group), head_dim) : 0);
 }
 
 cudaError_t enqueue_attention(const Pool& kv, const Batch& b, const AttnCall& c, const Rows& q, const Rows& out,
@@ -704,15 +738,45 @@ cudaError_t enqueue_attention(const Pool& kv, const Batch& b, const AttnCall& c,
     a.group = c.n_head / kv.n_kv;
     a.causal = c.causal;
     a.scale_log2 = c.scale * 1.4426950408889634f;
-    a.rows_lo = 0;
-    a.rows_hi = 0x7fffffff;
-    const int mt = (long long)b.max_q * a.group <= 16 ? 1 : 2;
-    a.parts.info = static_cast<PartInfo*>(c.workspace);
+    const bool bf16 = c.dtype == QWEN2_DTYPE_BF16;
+    TcMaps maps;
+    Plan plan = plan_of(b, kv, c.n_head, tensor_kernel(kv, c.n_head, c.format, c.scale));
+    if (plan.tc && !tc_encode(maps, kv, c, q, b.n_rows)) plan = plan_of(b, kv, c.n_head, false);
+    JoinArgs j{};
+    j.out = out;
+    j.lse = c.lse;
+    j.n_head = c.n_head;
+    j.group = a.group;
+    cudaError_t e = cudaSuccess;
+    char* ws = static_cast<char*>(c.workspace);
+    if (plan.tile) {
+        a.tile = plan.tile;
+        a.rows_lo = 0;
+        a.rows_hi = plan.few;
+        a.parts.info = reinterpret_cast<PartInfo*>(ws);
+        int* g = &j.n_cta[0];
+        if (c.head_dim == 64) e = bf16 ? launch_kind<64, true>(a, c.format, g, n_sm, st) : launch_kind<64, false>(a, c.format, g, n_sm, st);
+        else e = bf16 ? launch_kind<128, true>(a, c.format, g, n_sm, st) : launch_kind<128, false>(a, c.format, g, n_sm, st);
+        if (e != cudaSuccess) return e;
+        j.parts[0] = a.parts;
+        ws += parts_bytes(j.n_cta[0], plan.tile, c.head_dim);
+    }
+    if (plan.tc) {
+        a.tile = tc_tile_rows(a.group);
+        a.rows_lo = plan.tile ? plan.few : 0;
+        a.rows_hi = 0x7fffffff;
+        a.parts = carve_parts(ws, n_sm, a.tile);
+        e = enqueue_attention_tc(maps, a, c.head_dim, bf16, n_sm, plan.tile != 0, st);
+        if (e != cudaSuccess) return e;
+        j.parts[1] = a.parts;
+        j.n_cta[1] = n_sm;
+    }
+    const dim3 grid(j.n_cta[0] + j.n_cta[1], 16);
     if (c.head_dim == 64)
-        return c.dtype == QWEN2_DTYPE_BF16 ? launch_kind<64, true>(a, c.format, mt, n_sm, st)
-                                           : launch_kind<64, false>(a, c.format, mt, n_sm, st);
-    return c.dtype == QWEN2_DTYPE_BF16 ? launch_kind<128, true>(a, c.format, mt, n_sm, st)
-                                       : launch_kind<128, false>(a, c.format, mt, n_sm, st);
+        return bf16 ? launch_pdl(k_attn_join<64, true>, grid, dim3(128), 0, st, j)
+                    : launch_pdl(k_attn_join<64, false>, grid, dim3(128), 0, st, j);
+    return bf16 ? launch_pdl(k_attn_join<128, true>, grid, dim3(128), 0, st, j)
+                : launch_pdl(k_attn_join<128, false>, grid, dim3(128), 0, st, j);
 }
 
 }  // namespace paged

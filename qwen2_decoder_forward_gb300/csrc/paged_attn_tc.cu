@@ -1,0 +1,682 @@
+// Attention over the paged cache for chunks and prompts: the products on
+// tcgen05, K, V and the queries by TMA.  16-bit pages.
+//
+//   o_i = sum_j w_ij v_j / sum_j w_ij,   w_ij = 2^(s_ij - m_i),
+//   s_ij = scale log2(e) q_i . k_j,
+//
+// one pass over the keys with a running reference m_i of each row: any m_i
+// gives the same quotient, so m_i is moved up to the row's maximum (and the
+// accumulator rescaled) only when that has grown by more than 2^8 since; the
+// weights then stay below 2^8, far inside f16, and rescales are rare.
+//
+// A CTA (one per SM, persistent over its part of the work list, paged.cuh)
+// takes a tile of two 128-row halves A and B that share every K and V tile:
+// each half is R = 128 / group rows of the sequence with the group's heads
+// packed (a TMA box [R][group][64] lands as consecutive 128-byte rows), so a
+// K / V tile is read once for 2 R rows of all the group's heads.  Per unit of
+// 128 positions and half:  S = Q K^T into 128 columns of TMEM;
+// thread i of the half's warpgroup owns row i,
+// takes S into registers, writes P = 2^(s - m) as 16-bit pairs back to TMEM,
+// and the tensor core takes P from there: O += P V.  While the warpgroup of
+// one half is at its softmax, the products of the other half run.
+//
+// Warps: 0-3 softmax of A, 4-7 of B, 8 issues the products, 9 feeds (10 and 11
+// fill the third warpgroup).  TMEM
+// (512 columns): S_A, S_B at 0 and 128; O_A, O_B from 256; P in columns of
+// its own for head_dim 64, over its own S for head_dim 128, where S of the
+// next unit is issued once P V has completed.
+//
+// V is the [position][dim] tile as it lies in the pages: an MN-major B
+// operand, so nothing is transposed.  Positions of the last unit that are no
+// keys are zeroed in V (0 * NaN) and masked in S.
+#include <cuda.h>
+
+#include "paged.cuh"
+#include "paged.h"
+#include "sm100.cuh"
+#include "tmap.h"
+
+namespace qwen2 {
+namespace paged {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kUnit = 128;                 // positions per unit
+constexpr int kThreads = 384;
+// Registers per thread: the softmax warps hold a row of S each.  Launched with
+// 168 (64,512 in all): 2 * 128 * 200 + 128 * 104 = 64,512.
+constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
+constexpr int kMaxStages = 12;
+constexpr int kHalfBytes = 128 * 128;      // 128 rows of 64 16-bit elements
+constexpr uint32_t kTmemCols = 512;
+constexpr float kSlack = 8.f;              // log2 of the growth that is left in the weights
+
+struct TcSmem {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], tail, drain;
+    unsigned bad[8];                       // per unit (mod 8): its positions in bad pages, 16 per bit
+    uint32_t tmem_slot;
+    int abort;
+};
+constexpr int kHead = 1024;                // TcSmem, in front of the 1024-byte aligned tiles
+static_assert(sizeof(TcSmem) <= kHead, "");
+
+struct TcArgs {
+    AttnArgs a;
+    int sub;              // packed rows of a half: R * group
+    int sub_rows;         // R
+    int stages;           // ring stages of one K or V tile
+    int kv_rank[3];       // tensor-map dims (1..3) of position, head, page
+    int min_units;
+};
+
+__device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity, TcSmem& sm, int* guard) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_ns();
+    for (;;) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
+        if (global_ns() - t0 > kWaitNs) {
+            sm.abort = 1;
+            raise_guard(guard, kGuardTimeout);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+        "%5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// Descriptor of a V tile as B operand with N = dims contiguous (MN-major,
+// 128-byte swizzle): 64-dim halves kHalfBytes apart (leading offset), groups
+// of 8 positions 1024 bytes apart (stride offset).
+__device__ __forceinline__ uint64_t desc_mn128(uint32_t saddr) {
+    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(kHalfBytes >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// kind::f16 instruction descriptor: f32 accumulator, A and B f16 or bf16, B
+// K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc16(int M, int N, bool bf16, bool b_mn) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[tmem] . B[smem], issued by one thread.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 columns of this thread's TMEM lane, without waiting for them.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+// Waits for this thread's TMEM loads; no use of `r` moves above it.
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void pin32(uint32_t (&r)[32]) {
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                      "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]));
+    asm volatile("" : "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                      "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]));
+    asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int HD>
+struct Tmem {
+    static constexpr uint32_t s(int x) { return 128u * x; }
+    static constexpr uint32_t o(int x) { return 256u + (uint32_t)HD * x; }
+    static constexpr uint32_t p(int x) { return HD == 64 ? 384u + 64u * x : s(x); }
+};
+
+// a * b + c on two floats at once.
+__device__ __forceinline__ void fma2(float& x, float& y, float b, float c) {
+    asm("{\n\t.reg .b64 p, q, r;\n\t"
+        "mov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %2};\n\tmov.b64 r, {%3, %3};\n\t"
+        "fma.rn.f32x2 p, p, q, r;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "add.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Writes one finished row's 32 dims, or a partial's.
+template <bool BF16>
+__device__ __forceinline__ void put_row32(char* dst, const uint32_t (&o)[32], float inv) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = pack2<BF16>(__uint_as_float(o[8 * c + 2 * e]) * inv, __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
+        reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <int HD, bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_paged_attn_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcArgs args) {
+    using T = Tmem<HD>;
+    constexpr int kHalves = HD / 64;
+    constexpr int kTileBytes = kHalves * kHalfBytes;
+    const AttnArgs& a = args.a;
+    extern __shared__ unsigned char tc_smem_raw[];
+    const uint32_t pad = (1024u - (smem_addr(tc_smem_raw) & 1023u)) & 1023u;
+    TcSmem& sm = *reinterpret_cast<TcSmem*>(tc_smem_raw + pad);
+    const uint32_t q_tiles = smem_addr(&sm) + kHead;                 // A, B
+    const uint32_t ring = q_tiles + 2 * kTileBytes;
+    long long* prefix = reinterpret_cast<long long*>(tc_smem_raw + pad + kHead + (2 + args.stages) * kTileBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    pdl_launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < args.stages; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_empty, 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&sm.s_full[x], 1);
+            mbar_init(&sm.p_full[x], 128);
+            mbar_init(&sm.o_full[x], 1);
+        }
+        mbar_init(&sm.tail, 1);
+        mbar_init(&sm.drain, 1);
+        mbar_init_fence();
+        sm.abort = 0;
+    }
+    if (warp == 8) tmem_alloc(&sm.tmem_slot, kTmemCols);
+    if (warp == 9 && lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+    }
+    const WorkList work = build_work<kUnit>(a, prefix, args.min_units);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_slot;
+    long long left = work.end - work.begin;
+    const int slot0 = 2 * blockIdx.x;
+    bool wrote0 = false, wrote1 = false;
+    if (left > 0) {
+        Tile t = find_tile<kUnit>(a, work, work.begin, left);
+        if (warp < 8) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+            // ---- softmax of half x --------------------------------------------------
+            const int x = warp >> 2, rl = 32 * (warp & 3) + lane;
+            const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+            const uint32_t t_s = lanes + T::s(x), t_o = lanes + T::o(x), t_p = lanes + T::p(x);
+            const float sc = a.scale_log2;
+            unsigned n_s = 0;          // units of this half so far
+            unsigned unit = 0;         // units of the CTA before this tile
+            bool ok = true;
+            while (ok) {
+                const int packed0 = t.t * a.tile, packed = t.q.n * a.group;
+                const int i = packed0 + x * args.sub + rl;
+                const bool live = rl < args.sub && i < packed;
+                if (packed0 + x * args.sub < packed) {
+                    const int lim = live ? min(row_limit(a, t.q, i), t.keys - 1) : t.keys - 1;
+                    const int sure = min(row_limit(a, t.q, packed0 + x * args.sub), t.keys - 1);
+                    float m = -INFINITY, l0 = 0.f, l1 = 0.f;
+                    for (int u = 0; u < t.n; ++u, ++n_s) {
+                        const int key0 = (t.u0 + u) * kUnit;
+                        ok = __all_sync(0xffffffffu, wait(&sm.s_full[x], n_s & 1, sm, a.b.guard));
+                        if (!ok) break;
+                        tc_fence_after();
+                        uint32_t s[4][32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld32_async(t_s + 32 * c, s[c]);
+                        const unsigned bad = sm.bad[(unit + u) & 7];
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) pin32(s[c]);
+                        if (key0 + kUnit - 1 > sure || bad) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (key0 + 32 * c + e > lim || (bad >> (2 * c + e / 16) & 1)) s[c][e] = 0xff800000u;
+                        }
+                        float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2)
+                                v[e / 2 & 3] = max3(v[e / 2 & 3], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+                        const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * sc;
+                        // A new reference once the maximum has outgrown the old one.
+                        const bool move = top > m + kSlack;
+                        float corr = 1.f;
+                        if (move) {
+                            corr = ex2(m - top);
+                            m = top;
+                            l0 *= corr;
+                            l1 *= corr;
+                        }
+                        if (u > 0 && __any_sync(0xffffffffu, move)) {
+                            ok = __all_sync(0xffffffffu, wait(&sm.o_full[x], (n_s - 1) & 1, sm, a.b.guard));
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < HD / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32_async(t_o + 32 * c, o);
+                                tmem_ld_wait();
+                                pin32(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                                tmem_st32(t_o + 32 * c, o);
+                            }
+                        }
+                        const float base = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t p[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                float y = __uint_as_float(s[2 * c + e / 16][2 * e % 32]);
+                                float z = __uint_as_float(s[2 * c + e / 16][2 * e % 32 + 1]);
+                                fma2(y, z, sc, base);
+                                y = ex2(y);
+                                z = ex2(z);
+                                add2(l0, l1, y, z);
+                                p[e] = pack2<BF16>(y, z);
+                            }
+                            tmem_st32(t_p + 32 * c, p);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                        mbar_arrive(&sm.p_full[x]);
+                    }
+                    if (!ok) break;
+                    // ---- the half's rows ------------------------------------------------
+                    ok = __all_sync(0xffffffffu, wait(&sm.o_full[x], (n_s - 1) & 1, sm, a.b.guard));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const float l = l0 + l1;
+                    const bool begins = t.u0 == 0, ends = t.u0 + t.n >= t.units;
+                    const int slot = slot0 + (begins ? 1 : 0), r = x * args.sub + rl;
+                    if (begins && ends) {
+                        const float inv = l == 0.f ? 0.f : 1.f / l;
+                        const int row = t.q.q0 + i / a.group, qh = t.head * a.group + i % a.group;
+                        char* dst = a.out.data + (long long)row * a.out.row_bytes + (long long)qh * a.out.head_bytes;
+#pragma unroll
+                        for (int c = 0; c < HD / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32_async(t_o + 32 * c, o);
+                            tmem_ld_wait();
+                            pin32(o);
+                            if (live) put_row32<BF16>(dst + 64 * c, o, inv);
+                        }
+                        if (live && a.lse)
+                            a.lse[(long long)row * a.n_head + qh] =
+                                l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                    } else {
+                        float* po = a.parts.o + ((long long)slot * a.parts.rows + r) * HD;
+#pragma unroll
+                        for (int c = 0; c < HD / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32_async(t_o + 32 * c, o);
+                            tmem_ld_wait();
+                            pin32(o);
+                            if (live)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    reinterpret_cast<uint4*>(po + 32 * c)[e] =
+                                        make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                        if (live) {
+                            a.parts.ml[(long long)slot * 2 * a.parts.rows + r] = m;
+                            a.parts.ml[((long long)slot * 2 + 1) * a.parts.rows + r] = l;
+                        }
+                        if (begins) wrote1 = true;
+                        else wrote0 = true;
+                        if (tid == 0) {
+                            PartInfo pi;
+                            pi.q0 = t.q.q0;
+                            pi.packed0 = packed0;
+                            pi.packed_end = min(packed0 + a.tile, packed);
+                            pi.head = t.head;
+                            pi.state = kPartUsed | (ends ? kPartLast : 0);
+                            a.parts.info[slot] = pi;
+                        }
+                    }
+                    tc_fence_before();
+                }
+                unit += t.n;
+                left -= t.n;
+                if (left <= 0) break;
+                next_tile<kUnit>(a, work, t, left);
+            }
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        }
+        if (warp == 8) {
+            // ---- products -------------------------------------------------------------
+            if (lane == 0) {
+                constexpr uint32_t id_s = idesc16(128, kUnit, BF16, false), id_o = idesc16(128, HD, BF16, true);
+                unsigned n_u[2] = {0, 0}, seg = 0, ent = 0;
+                bool ok = true;
+                const auto stage_of = [&](unsigned e) { return e % (unsigned)args.stages; };
+                const auto landed = [&](unsigned e) {
+                    ok = ok && wait(&sm.full[stage_of(e)], (e / (unsigned)args.stages) & 1, sm, a.b.guard);
+                };
+                // S of half x against the K tile of ring entry e.
+                const auto issue_s = [&](int x, unsigned e) {
+                    if (n_u[x])
+                        ok = ok && wait(&sm.o_full[x], (n_u[x] - 1) & 1, sm, a.b.guard);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint64_t qd = desc_sw128(q_tiles + x * kTileBytes);
+                    const uint64_t kd = desc_sw128(ring + stage_of(e) * kTileBytes);
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k) {
+                        const uint32_t off = (uint32_t)((k / 4) * kHalfBytes + (k % 4) * 32) >> 4;
+                        mma_f16(tmem + T::s(x), qd + off, kd + off, id_s, k != 0 ? 1u : 0u);
+                    }
+                    mma_commit(&sm.s_full[x]);
+                };
+                while (ok) {
+                    const int halves = t.t * a.tile + args.sub < t.q.n * a.group ? 2 : 1;
+                    ok = wait(&sm.q_full, seg & 1, sm, a.b.guard);
+                    ++seg;
+                    landed(ent);
+                    for (int x = 0; x < halves && ok; ++x) issue_s(x, ent);
+                    if (!ok) break;
+                    mma_commit(&sm.empty[stage_of(ent)]);
+                    if (t.n == 1) mma_commit(&sm.q_empty);
+                    ++ent;
+                    for (int u = 0; u < t.n; ++u) {
+                        const unsigned ev = ent;           // V of this unit; K of the next one follows
+                        landed(ev);
+                        if (u + 1 < t.n) landed(ev + 1);
+                        for (int x = 0; x < halves; ++x) {
+                            ok = ok && wait(&sm.p_full[x], n_u[x] & 1, sm, a.b.guard);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t vd = desc_mn128(ring + stage_of(ev) * kTileBytes);
+#pragma unroll
+                            for (int k = 0; k < kUnit / 16; ++k)
+                                mma_ts(tmem + T::o(x), tmem + T::p(x) + 8 * k, vd + (2048 * k >> 4), id_o,
+                                       u > 0 || k > 0 ? 1u : 0u);
+                            mma_commit(&sm.o_full[x]);
+                            ++n_u[x];
+                            if (u + 1 < t.n) issue_s(x, ev + 1);
+                        }
+                        if (!ok) break;
+                        mma_commit(&sm.empty[stage_of(ev)]);
+                        ++ent;
+                        if (u + 1 < t.n) {
+                            mma_commit(&sm.empty[stage_of(ev + 1)]);
+                            if (u + 2 == t.n) mma_commit(&sm.q_empty);
+                            ++ent;
+                        }
+                    }
+                    left -= t.n;
+                    if (left <= 0 || !ok) break;
+                    next_tile<kUnit>(a, work, t, left);
+                }
+                if (!ok) {   // products in flight end before the tensor memory is given back
+                    mma_commit(&sm.drain);
+                    mbar_wait(&sm.drain, 0, kWaitNs);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            // ---- feed -------------------------------------------------------------------
+            const int page_rows = 1 << a.kv.page_shift, box = min(page_rows, kUnit), boxes = kUnit / box;
+            const int p = lane / kHalves, h = lane % kHalves;
+            unsigned ent = 0, seg = 0, unit = 0, n_tail = 0;
+            bool ok = true;
+            while (ok) {
+                const int halves = t.t * a.tile + args.sub < t.q.n * a.group ? 2 : 1;
+                if (seg) ok = __all_sync(0xffffffffu, wait(&sm.q_empty, (seg - 1) & 1, sm, a.b.guard));
+                if (!ok) break;
+                if (lane == 0) {
+                    mbar_expect_tx(&sm.q_full, (unsigned)(halves * kHalves * args.sub * 128));
+                    for (int x = 0; x < halves; ++x)
+                        for (int c = 0; c < kHalves; ++c)
+                            tma_load_3d(q_tiles + x * kTileBytes + c * kHalfBytes, &tm_q, 64 * c, t.head * a.group,
+                                        t.q.q0 + (2 * t.t + x) * args.sub_rows, &sm.q_full);
+                }
+                __syncwarp();
+                ++seg;
+                for (int u = 0; u < t.n && ok; ++u, ++unit) {
+                    const int key0 = (t.u0 + u) * kUnit, key = key0 + p * box;
+                    int page = -1;
+                    bool is_bad = false;
+                    if (p < boxes && key < t.keys) {
+                        page = __ldg(a.b.pages + (long long)t.s * a.b.pages_stride + (key >> a.kv.page_shift));
+                        if ((unsigned)page >= (unsigned)a.kv.n_pages) {
+                            is_bad = true;
+                            page = -1;
+                            raise_guard(a.b.guard, QWEN2_GUARD_PAGE);
+                        }
+                    }
+                    const unsigned bad = __reduce_or_sync(
+                        0xffffffffu, is_bad ? ((1u << (box / 16)) - 1) << (p * box / 16) : 0u);
+                    const unsigned bytes = (unsigned)(__popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128);
+                    const bool whole = key0 + kUnit <= t.keys && !bad;
+                    int at[3];
+                    at[args.kv_rank[0]] = key & (page_rows - 1);
+                    at[args.kv_rank[1]] = t.head;
+                    at[args.kv_rank[2]] = page;
+                    for (int kv = 0; kv < 2 && ok; ++kv, ++ent) {
+                        const unsigned st = ent % (unsigned)args.stages, round = ent / (unsigned)args.stages;
+                        if (round) ok = __all_sync(0xffffffffu, wait(&sm.empty[st], (round - 1) & 1, sm, a.b.guard));
+                        if (!ok) break;
+                        const uint32_t tile = ring + st * kTileBytes;
+                        uint64_t* bar = kv && !whole ? &sm.tail : &sm.full[st];
+                        if (lane == 0) {
+                            if (!kv) sm.bad[unit & 7] = bad;
+                            mbar_expect_tx(bar, bytes);
+                        }
+                        __syncwarp();
+                        if (page >= 0)
+                            tma_load_4d(tile + h * kHalfBytes + p * box * 128, kv ? &tm_v : &tm_k, 64 * h, at[0], at[1],
+                                        at[2], bar);
+                        if (kv && !whole) {
+                            // Positions that are no keys: zeros in V.
+                            ok = __all_sync(0xffffffffu, wait(&sm.tail, n_tail & 1, sm, a.b.guard));
+                            ++n_tail;
+                            if (!ok) {
+                                mbar_wait(&sm.tail, (n_tail - 1) & 1, kWaitNs);
+                                break;
+                            }
+                            for (int r = lane; r < kUnit; r += 32)
+                                if (key0 + r >= t.keys || (bad >> (r / 16) & 1))
+                                    for (int c = 0; c < 8 * kHalves; ++c)
+                                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                                         tile + (c / 8) * kHalfBytes + r * 128 + (c % 8) * 16),
+                                                     "r"(0)
+                                                     : "memory");
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sm.full[st]);
+                        }
+                    }
+                }
+                left -= t.n;
+                if (left <= 0 || !ok) break;
+                next_tile<kUnit>(a, work, t, left);
+            }
+            if (!ok) {   // copies in flight land before the shared memory is given back
+                for (unsigned e = ent > (unsigned)args.stages ? ent - args.stages : 0; e < ent; ++e)
+                    mbar_wait(&sm.full[e % (unsigned)args.stages], (e / (unsigned)args.stages) & 1, kWaitNs);
+                if (seg) mbar_wait(&sm.q_full, (seg - 1) & 1, kWaitNs);
+            }
+            __syncwarp();
+        }
+    }
+    if (tid == 0) {
+        if (!wrote0) a.parts.info[slot0].state = kPartNone;
+        if (!wrote1) a.parts.info[slot0 + 1].state = kPartNone;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, kTmemCols);
+    // The few-rows kernel before this one may still run: whoever waits for this
+    // kernel waits for both.
+    pdl_wait();
+}
+
+// A pool's tensor map: 64 dims of `box` positions of one head and page per
+// copy.  The dims stand in the order of their strides, rank[] says where
+// position, head and page went.
+bool encode_pool(CUtensorMap* m, const char* base, const Pool& kv, int head_dim, bool bf16, int (&rank)[3]) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const int page = 1 << kv.page_shift;
+    long long stride[3] = {kv.token_bytes, kv.head_bytes, kv.page_bytes};
+    const unsigned long long size[3] = {(unsigned long long)page, (unsigned long long)kv.n_kv,
+                                        (unsigned long long)kv.n_pages};
+    // A dim of one element may have any stride.
+    for (int i = 0; i < 3; ++i)
+        if (size[i] == 1) stride[i] = (long long)head_dim * 2 << 20;
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (stride[order[j]] > stride[order[j + 1]]) {
+                const int x = order[j];
+                order[j] = order[j + 1];
+                order[j + 1] = x;
+            }
+    cuuint64_t dims[4] = {(cuuint64_t)head_dim, 1, 1, 1}, strides[3];
+    cuuint32_t box[4] = {64, 1, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        const int d = order[i];
+        rank[d] = i;
+        dims[1 + i] = size[d];
+        strides[i] = (cuuint64_t)stride[d];
+        if (d == 0) box[1 + i] = (cuuint32_t)(page < kUnit ? page : kUnit);
+    }
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+               const_cast<char*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_q(CUtensorMap* m, const Rows& q, int n_rows, int n_head, int group, int sub_rows, int head_dim, bool bf16) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)n_head, (cuuint64_t)n_rows};
+    const cuuint64_t strides[2] = {n_head > 1 ? (cuuint64_t)q.head_bytes : (cuuint64_t)head_dim * 2,
+                                   n_rows > 1 ? (cuuint64_t)q.row_bytes : (cuuint64_t)head_dim * 2 * n_head};
+    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)sub_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, q.data, dims, strides,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int HD, bool BF16>
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, TcArgs& args, int n_sm,
+                   bool chained, cudaStream_t st) {
+    constexpr int kTileBytes = HD / 64 * kHalfBytes;
+    auto kern = k_paged_attn_tc<HD, BF16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    const int prefix = 8 * (args.a.b.n_seq + 1), room = 227 * 1024 - 1024 - kHead - prefix - 2 * kTileBytes;
+    args.stages = min(kMaxStages, room / kTileBytes);
+    const size_t smem = 1024 + kHead + (size_t)(2 + args.stages) * kTileBytes + prefix;
+    if (chained) return launch_pdl(kern, dim3(n_sm), dim3(kThreads), smem, st, q, k, v, args);
+    kern<<<n_sm, kThreads, smem, st>>>(q, k, v, args);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int tc_tile_rows(int group) { return 2 * (128 / group) * group; }
+
+bool tc_encode(TcMaps& m, const Pool& kv, const AttnCall& c, const Rows& q, int n_rows) {
+    const bool bf16 = c.dtype == QWEN2_DTYPE_BF16;
+    const int group = c.n_head / kv.n_kv;
+    int rank_v[3];
+    return encode_pool(&m.k, kv.k, kv, c.head_dim, bf16, m.kv_rank) &&
+           encode_pool(&m.v, kv.v, kv, c.head_dim, bf16, rank_v) &&
+           encode_q(&m.q, q, n_rows, c.n_head, group, 128 / group, c.head_dim, bf16);
+}
+
+cudaError_t enqueue_attention_tc(const TcMaps& m, const AttnArgs& a, int head_dim, bool bf16, int n_sm, bool chained,
+                                 cudaStream_t st) {
+    TcArgs args{};
+    args.a = a;
+    args.sub = a.tile / 2;
+    args.sub_rows = args.sub / a.group;
+    for (int i = 0; i < 3; ++i) args.kv_rank[i] = m.kv_rank[i];
+    args.min_units = 2;
+    if (head_dim == 64)
+        return bf16 ? launch<64, true>(m.q, m.k, m.v, args, n_sm, chained, st)
+                    : launch<64, false>(m.q, m.k, m.v, args, n_sm, chained, st);
+    return bf16 ? launch<128, true>(m.q, m.k, m.v, args, n_sm, chained, st)
+                : launch<128, false>(m.q, m.k, m.v, args, n_sm, chained, st);
+}
+
+}  // namespace paged
+}  // namespace qwen2
