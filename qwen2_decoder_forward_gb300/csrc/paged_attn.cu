@@ -600,9 +600,11 @@ struct JoinArgs {
 };
 
 // Adds up the tile that begins in a CTA's slot 1 and goes on in the slots 0 of
-// the CTAs after it: rows blockIdx.y, blockIdx.y + gridDim.y, ... of it, a
-// block per row, its warps taking the parts in turn.  blockIdx.x counts the
-// CTAs of the first kernel, then those of the second.
+// the CTAs after it; blockIdx.x counts the CTAs of the first kernel, then those
+// of the second.  Few parts: a warp per row, gridDim.y blocks share the rows.
+// Many parts (a long sequence alone): the block's four warps take a row's
+// parts in turn.  The grid is small on purpose: most CTAs left no open tile,
+// and 7,296 blocks that only look cost 6 us, 912 cost less than 2.
 template <int HD, bool BF16>
 __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ JoinArgs a) {
     constexpr int kV = HD / 32;     // dims per lane
@@ -616,53 +618,75 @@ __global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ JoinA
     if (first.state == kPartNone) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rows = parts.rows;
-    // Parts: slot 2 c0 + 1, then slots 2 c of the following CTAs up to the last.
+    // Parts: slot 2 c0 + 1, then slots 2 c of the following CTAs up to the one
+    // that ends the tile; 32 CTAs are looked at at a time.
     int n = 1;
-    for (int c = c0 + 1;; ++n, ++c) {
-        if (c >= n_cta) break;
-        const int st = parts.info[2 * c].state;
-        if (st == kPartNone) break;
-        if (st & kPartLast) {
-            ++n;
+    for (int c = c0 + 1; c < n_cta; c += 32) {
+        const int st = c + lane < n_cta ? parts.info[2 * (c + lane)].state : kPartNone;
+        const unsigned stop = __ballot_sync(0xffffffffu, st == kPartNone || (st & kPartLast));
+        if (stop) {
+            const int k = __ffs(stop) - 1;
+            n += k + (__shfl_sync(0xffffffffu, st, k) != kPartNone);
             break;
         }
+        n += 32;
     }
-    for (int r = blockIdx.y; first.packed0 + r < first.packed_end; r += gridDim.y) {
-        const auto slot = [&](int k) { return k == 0 ? 2 * c0 + 1 : 2 * (c0 + k); };
-        float top = -INFINITY;
-        for (int k = lane; k < n; k += 32) top = fmaxf(top, parts.ml[(long long)slot(k) * 2 * rows + r]);
-        top = warp_max(top);
-        const float base = top == -INFINITY ? 0.f : top;
-        float acc[kV], sum = 0.f;
+    const bool together = n > 8;
+    const int step = together ? 1 : 4;
+    const auto slot = [&](int k) { return k == 0 ? 2 * c0 + 1 : 2 * (c0 + k); };
+    for (int r0 = blockIdx.y * step; first.packed0 + r0 < first.packed_end; r0 += gridDim.y * step) {
+        const int r = together ? r0 : r0 + warp;
+        const bool in = first.packed0 + r < first.packed_end;
+        float top = -INFINITY, sum = 0.f, acc[kV];
 #pragma unroll
         for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+        if (in) {
+            for (int k = lane; k < n; k += 32) top = fmaxf(top, parts.ml[(long long)slot(k) * 2 * rows + r]);
+            top = warp_max(top);
+            const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll 4
-        for (int k = warp; k < n; k += 4) {
-            const float* ml = parts.ml + (long long)slot(k) * 2 * rows + r;
-            const float w = ex2(ml[0] - base);
-            sum = fmaf(ml[rows], w, sum);
-            const float* o = parts.o + ((long long)slot(k) * rows + r) * HD + kV * lane;
-#pragma unroll
-            for (int e = 0; e < kV; ++e) acc[e] = fmaf(o[e], w, acc[e]);
+            for (int k = together ? warp : 0; k < n; k += step == 1 ? 4 : 1) {
+                const float* ml = parts.ml + (long long)slot(k) * 2 * rows + r;
+                const float w = ex2(ml[0] - base);
+                sum = fmaf(ml[rows], w, sum);
+                const float* o = parts.o + ((long long)slot(k) * rows + r) * HD + kV * lane;
+                if constexpr (kV == 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(o);
+                    acc[0] = fmaf(x.x, w, acc[0]);
+                    acc[1] = fmaf(x.y, w, acc[1]);
+                    acc[2] = fmaf(x.z, w, acc[2]);
+                    acc[3] = fmaf(x.w, w, acc[3]);
+                } else {
+                    const float2 x = *reinterpret_cast<const float2*>(o);
+                    acc[0] = fmaf(x.x, w, acc[0]);
+                    acc[1] = fmaf(x.y, w, acc[1]);
+                }
+            }
         }
+        if (together) {
 #pragma unroll
-        for (int e = 0; e < kV; ++e) so[warp][kV * lane + e] = acc[e];
-        if (lane == 0) sl[warp] = sum;
-        __syncthreads();
+            for (int e = 0; e < kV; ++e) so[warp][kV * lane + e] = acc[e];
+            if (lane == 0) sl[warp] = sum;
+            __syncthreads();
+            sum = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+#pragma unroll
+            for (int e = 0; e < kV; ++e) {
+                const int d = kV * lane + e;
+                acc[e] = (so[0][d] + so[1][d]) + (so[2][d] + so[3][d]);
+            }
+            __syncthreads();
+        }
+        if (!in || (together && warp)) continue;
         const int i = first.packed0 + r;
         const int row = first.q0 + i / a.group, qh = first.head * a.group + i % a.group;
-        sum = (sl[0] + sl[1]) + (sl[2] + sl[3]);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        if (threadIdx.x < HD / 2) {
-            const int d = 2 * threadIdx.x;
-            const float x = ((so[0][d] + so[1][d]) + (so[2][d] + so[3][d])) * inv;
-            const float y = ((so[0][d + 1] + so[1][d + 1]) + (so[2][d + 1] + so[3][d + 1])) * inv;
-            *reinterpret_cast<uint32_t*>(a.out.data + (long long)row * a.out.row_bytes +
-                                         (long long)qh * a.out.head_bytes + 4 * threadIdx.x) = pack2<BF16>(x, y);
-        }
-        if (a.lse && threadIdx.x == 0)
+        char* dst = a.out.data + (long long)row * a.out.row_bytes + (long long)qh * a.out.head_bytes + 2 * kV * lane;
+        if constexpr (kV == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv));
+        else
+            *reinterpret_cast<uint32_t*>(dst) = pack2<BF16>(acc[0] * inv, acc[1] * inv);
+        if (a.lse && lane == 0)
             a.lse[(long long)row * a.n_head + qh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-        __syncthreads();
     }
 }
 
@@ -679,6 +703,11 @@ cudaError_t launch_few(AttnArgs& a, int* grid, int n_sm, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int by_smem = (int)(228 * 1024 / (smem + 1024));
     *grid = n_sm * max(1, min(by_smem, MT == 1 ? kMaxCtasPerSm : 2));
+    // No more CTAs than the batch can have units.
+    const long long tiles = ((long long)a.b.max_q * a.group + a.tile - 1) / a.tile;
+    const long long units = (((long long)a.b.max_pages << a.kv.page_shift) + kUnit - 1) / kUnit;
+    if (a.b.n_seq * tiles * a.kv.n_kv < *grid)
+        *grid = (int)min((long long)*grid, a.b.n_seq * tiles * a.kv.n_kv * units);
     a.parts = carve_parts(a.parts.info, *grid, 16 * MT);
     kern<<<*grid, kThreads, smem, st>>>(a);
     return cudaGetLastError();
@@ -771,7 +800,7 @@ cudaError_t enqueue_attention(const Pool& kv, const Batch& b, const AttnCall& c,
         j.parts[1] = a.parts;
         j.n_cta[1] = n_sm;
     }
-    const dim3 grid(j.n_cta[0] + j.n_cta[1], 16);
+    const dim3 grid(j.n_cta[0] + j.n_cta[1], plan.tc ? 8 : 2);
     if (c.head_dim == 64)
         return bf16 ? launch_pdl(k_attn_join<64, true>, grid, dim3(128), 0, st, j)
                     : launch_pdl(k_attn_join<64, false>, grid, dim3(128), 0, st, j);

@@ -83,15 +83,21 @@ def _check(rc: int):
 
 _dtypes = {}     # torch dtype -> QWEN2_DTYPE_*
 _formats = {}    # torch dtype -> QWEN2_KV_*
+_t = None        # torch, once it is needed
 
 
 def _types():
-    if not _dtypes:
+    global _t, _raw_stream
+    if _t is None:
         import torch
         _formats.update({torch.float16: KV_F16, torch.bfloat16: KV_BF16, torch.int8: KV_INT8,
                          torch.float8_e4m3fn: KV_E4M3})
         _dtypes.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
-    return _dtypes
+        # The current stream's pointer, without building a Stream object for it.
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _t = torch
+    return _t
 
 
 def rope_table(rows: int, rotary_dim: int, theta: float = 1e6, kind: int = ROPE_PLAIN, factor: float = 1.0,
@@ -126,7 +132,7 @@ class PagedKV:
         if self.format in (KV_INT8, KV_E4M3):
             want = (k.shape[0], k.shape[2], k.shape[1])
             for s in (k_scale, v_scale):
-                if s is None or tuple(s.shape) != want or str(s.dtype) != "torch.float32" or \
+                if s is None or tuple(s.shape) != want or s.dtype != _t.float32 or \
                         s.device != k.device or not s.is_contiguous():
                     raise ValueError("8-bit pages need contiguous f32 scales [n_pages, n_kv_head, page_size]")
         else:
@@ -138,13 +144,12 @@ class PagedKV:
                            v_scale.data_ptr() if v_scale is not None else None, self.format, self.n_pages,
                            self.page_size, self.n_kv_head, self.head_dim, *k.stride()[:3])
         self._at = ctypes.addressof(self._c)
-        self._shape = (self.n_kv_head, self.head_dim)
+        self._index = k.device.index
 
     @classmethod
     def zeros(cls, n_pages: int, page_size: int, n_kv_head: int, head_dim: int, format: int, device="cuda"):
         """A pool of zeroed, head-major pages."""
-        import torch
-        _types()
+        torch = _types()
         dtype = next(d for d, f in _formats.items() if f == format)
         k, v = (torch.zeros((n_pages, n_kv_head, page_size, head_dim), dtype=torch.int8 if dtype.itemsize == 1 else dtype,
                             device=device).view(dtype).permute(0, 2, 1, 3) for _ in range(2))
@@ -163,8 +168,7 @@ class PagedBatch:
     anew and may be changed in place between them."""
 
     def __init__(self, q_start, kv_len, pages, max_q: int):
-        import torch
-        _types()
+        torch = _types()
         n = kv_len.shape[0] if kv_len.dim() == 1 else -1
         if n < 1 or tuple(q_start.shape) != (n + 1,) or pages.dim() != 2 or pages.shape[0] != n or pages.shape[1] < 1:
             raise ValueError("q_start must be [n_seq + 1], kv_len [n_seq] and pages [n_seq, max_pages]")
@@ -195,10 +199,13 @@ class PagedBatch:
             raise Qwen2Error(QWEN2_E_DEVICE_GUARD, f"device guard {code}: {names.get(code, 'unknown')}")
 
 
-def _rows(t, name: str, shape, device):
-    """The descriptor of a [rows, heads, head_dim] tensor; shape: (heads or None, head_dim)."""
-    if t.dim() != 3 or t.shape[2] != shape[1] or (shape[0] is not None and t.shape[1] != shape[0]):
-        raise ValueError(f"{name} must be [rows, {shape[0] if shape[0] is not None else 'heads'}, {shape[1]}]")
+def _rows(t, name: str, heads, hd: int, rows, device):
+    """The descriptor of a [rows, heads, head_dim] tensor (rows, heads: None for any)."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != hd or (heads is not None and shape[1] != heads) or \
+            (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {'heads' if heads is None else heads}, {hd}], "
+                         f"not {list(shape)}")
     dt = _dtypes.get(t.dtype)
     if dt is None:
         raise ValueError(f"{name}: {t.dtype} is not supported")
@@ -210,26 +217,32 @@ def _rows(t, name: str, shape, device):
     return _Rows(t.data_ptr(), dt, rs, hs)
 
 
-def _on_stream(kv, batch, stream, call):
-    """Runs ``call(stream pointer)`` with the pool's device current and, where
-    the caller names a stream, with that stream current, so that outputs and
-    workspaces are allocated for it."""
-    import torch
-    if batch.device != kv.device:
-        raise ValueError("the pool and the batch are on different devices")
-    if stream is not None:
-        if stream.device != kv.device:
+class _Call:
+    """The stream of a call: the pool's device current and, where the caller
+    names a stream, that stream current, so that outputs and workspaces are
+    allocated for it."""
+
+    def __init__(self, kv, batch, stream):
+        if batch.device != kv.device:
+            raise ValueError("the pool and the batch are on different devices")
+        if stream is not None and stream.device != kv.device:
             raise ValueError("the stream belongs to another device")
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
-    if torch.cuda.current_device() != kv.device.index:
-        with torch.cuda.device(kv.device):
-            return call(torch.cuda.current_stream().cuda_stream)
-    return call(torch.cuda.current_stream().cuda_stream)
+        self.guard = _t.cuda.stream(stream) if stream is not None else _t.cuda.device(kv.device)
+
+    def __enter__(self):
+        self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+
+def _plain(kv, batch, stream):
+    """Whether a call needs no change of stream or device."""
+    return stream is None and batch.device == kv.device and _t.cuda.current_device() == kv._index
 
 
 def _f32(t, name: str, shape, device):
-    if str(t.dtype) != "torch.float32" or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+    if t.dtype != _t.float32 or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous f32 tensor of shape {list(shape)} on {device}")
     return t.data_ptr()
 
@@ -244,44 +257,44 @@ def paged_write(kv: PagedKV, batch: PagedBatch, k, v, q=None, q_out=None, q_dtyp
     at each row's position, dims paired (i, i + rotary_dim / 2) or, if
     ``interleaved``, (2i, 2i + 1).  Queries come in ``q_dtype`` (default: the
     pages' type if 16-bit, else q's if 16-bit, else f16)."""
-    def call(st):
-        import torch
-        rows = k.shape[0]
-        rk, rv = _rows(k, "k", kv._shape, kv.device), _rows(v, "v", kv._shape, kv.device)
-        if v.shape[0] != rows:
-            raise ValueError("k and v must have the same rows")
-        out, n_head, rq, ro = None, 0, None, None
-        if q is not None:
-            if q.shape[0] != rows:
-                raise ValueError("q and k must have the same rows")
-            rq = _rows(q, "q", (None, kv.head_dim), kv.device)
-            n_head = q.shape[1]
-            out = q_out
-            if out is None:
-                dt = q_dtype or (kv.k.dtype if kv.format <= KV_BF16 else
-                                 q.dtype if q.dtype != torch.float32 else torch.float16)
-                out = torch.empty((rows, n_head, kv.head_dim), dtype=dt, device=kv.device)
-            ro = _rows(out, "q_out", (n_head, kv.head_dim), kv.device)
-            if out.shape[0] != rows:
-                raise ValueError("q_out and q must have the same rows")
-        elif q_out is not None or q_norm is not None:
-            raise ValueError("q_out and q_norm need q")
-        o = _WriteOpts(norm_eps=norm_eps)
+    if not _plain(kv, batch, stream):
+        with _Call(kv, batch, stream):
+            return paged_write(kv, batch, k, v, q, q_out, q_dtype, q_norm, k_norm, norm_eps, rope, interleaved)
+    dev, hd = kv.device, kv.head_dim
+    rk = _rows(k, "k", kv.n_kv_head, hd, None, dev)
+    rows = k.shape[0]
+    rv = _rows(v, "v", kv.n_kv_head, hd, rows, dev)
+    n_head, pq, po = 0, None, None
+    if q is not None:
+        rq = _rows(q, "q", None, hd, rows, dev)
+        n_head = q.shape[1]
+        if q_out is None:
+            dt = q_dtype or (kv.k.dtype if kv.format <= KV_BF16 else q.dtype if q.dtype != _t.float32 else _t.float16)
+            q_out = _t.empty((rows, n_head, hd), dtype=dt, device=dev)
+        ro = _rows(q_out, "q_out", n_head, hd, rows, dev)
+        pq, po = ctypes.addressof(rq), ctypes.addressof(ro)
+    elif q_out is not None or q_norm is not None:
+        raise ValueError("q_out and q_norm need q")
+    po_opts = None
+    if q_norm is not None or k_norm is not None or rope is not None:
+        o = _WriteOpts(None, None, norm_eps, None, 0, 0, 0)
         if q_norm is not None:
-            o.q_norm = _f32(q_norm, "q_norm", (kv.head_dim,), kv.device)
+            o.q_norm = _f32(q_norm, "q_norm", (hd,), dev)
         if k_norm is not None:
-            o.k_norm = _f32(k_norm, "k_norm", (kv.head_dim,), kv.device)
+            o.k_norm = _f32(k_norm, "k_norm", (hd,), dev)
         if rope is not None:
-            if rope.dim() != 3 or rope.shape[2] != 2:
+            shape = rope.shape
+            if len(shape) != 3 or shape[2] != 2:
                 raise ValueError("rope must be [positions, rotary_dim / 2, 2]")
-            o.rope = _f32(rope, "rope", tuple(rope.shape), kv.device)
-            o.rope_rows, o.rotary_dim, o.interleaved = rope.shape[0], 2 * rope.shape[1], int(interleaved)
-        batch._c.n_rows = rows
-        _check(_lib().qwen2_paged_write(kv._at, batch._at, ctypes.addressof(o), n_head,
-                                        ctypes.addressof(rq) if rq else None, ctypes.addressof(ro) if ro else None,
-                                        ctypes.addressof(rk), ctypes.addressof(rv), st))
-        return out
-    return _on_stream(kv, batch, stream, call)
+            o.rope = _f32(rope, "rope", shape, dev)
+            o.rope_rows, o.rotary_dim, o.interleaved = shape[0], 2 * shape[1], int(interleaved)
+        po_opts = ctypes.addressof(o)
+    batch._c.n_rows = rows
+    rc = _lib().qwen2_paged_write(kv._at, batch._at, po_opts, n_head, pq, po, ctypes.addressof(rk), ctypes.addressof(rv),
+                                  _raw_stream(kv._index))
+    if rc:
+        _check(rc)
+    return q_out
 
 
 def paged_read(kv: PagedKV, batch: PagedBatch, out_start, n_rows: int, dtype=None, k_out=None, v_out=None, stream=None):
@@ -289,25 +302,26 @@ def paged_read(kv: PagedKV, batch: PagedBatch, out_start, n_rows: int, dtype=Non
     row out_start[s] + p of (k, v), [n_rows, n_kv_head, head_dim] in ``dtype``
     (f32, f16 or bf16; default f32).  ``out_start``: int32 CUDA tensor
     [n_seq + 1]; rows outside the sequences are left as they were."""
-    def call(st):
-        import torch
-        if tuple(out_start.shape) != (batch.n_seq + 1,) or out_start.dtype != torch.int32 or \
-                out_start.device != kv.device or not out_start.is_contiguous():
-            raise ValueError("out_start must be a contiguous int32 tensor [n_seq + 1] on the pool's device")
-        if (k_out is None) != (v_out is None):
-            raise ValueError("k_out and v_out go together")
-        ko, vo = k_out, v_out
-        if ko is None:
-            shape = (n_rows, *kv._shape)
-            ko = torch.empty(shape, dtype=dtype or torch.float32, device=kv.device)
-            vo = torch.empty(shape, dtype=dtype or torch.float32, device=kv.device)
-        rk, rv = _rows(ko, "k_out", kv._shape, kv.device), _rows(vo, "v_out", kv._shape, kv.device)
-        if ko.shape[0] < n_rows or vo.shape[0] < n_rows:
-            raise ValueError("k_out and v_out need n_rows rows")
-        _check(_lib().qwen2_paged_read(kv._at, batch._at, out_start.data_ptr(), n_rows, ctypes.addressof(rk),
-                                       ctypes.addressof(rv), st))
-        return ko, vo
-    return _on_stream(kv, batch, stream, call)
+    if not _plain(kv, batch, stream):
+        with _Call(kv, batch, stream):
+            return paged_read(kv, batch, out_start, n_rows, dtype, k_out, v_out)
+    dev, heads, hd = kv.device, kv.n_kv_head, kv.head_dim
+    if out_start.shape != (batch.n_seq + 1,) or out_start.dtype != _t.int32 or out_start.device != dev or \
+            not out_start.is_contiguous():
+        raise ValueError("out_start must be a contiguous int32 tensor [n_seq + 1] on the pool's device")
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out go together")
+    if k_out is None:
+        k_out = _t.empty((n_rows, heads, hd), dtype=dtype or _t.float32, device=dev)
+        v_out = _t.empty((n_rows, heads, hd), dtype=dtype or _t.float32, device=dev)
+    rk, rv = _rows(k_out, "k_out", heads, hd, None, dev), _rows(v_out, "v_out", heads, hd, None, dev)
+    if k_out.shape[0] < n_rows or v_out.shape[0] < n_rows:
+        raise ValueError("k_out and v_out need n_rows rows")
+    rc = _lib().qwen2_paged_read(kv._at, batch._at, out_start.data_ptr(), n_rows, ctypes.addressof(rk),
+                                 ctypes.addressof(rv), _raw_stream(kv._index))
+    if rc:
+        _check(rc)
+    return k_out, v_out
 
 
 def paged_attention(kv: PagedKV, batch: PagedBatch, q, out=None, scale=None, causal: bool = True,
@@ -319,37 +333,40 @@ def paged_attention(kv: PagedKV, batch: PagedBatch, q, out=None, scale=None, cau
     the log of the sum of exp(scale q.k), -inf for a row without keys (whose o
     is 0).  ``scale``: default head_dim^-1/2.  ``workspace``: a uint8 CUDA
     tensor of ``paged_attention_workspace`` bytes (default: allocated here)."""
-    def call(st):
-        import torch
-        rows, n_head = q.shape[0], q.shape[1]
-        rq = _rows(q, "q", (None, kv.head_dim), kv.device)
-        o = torch.empty(q.shape, dtype=q.dtype, device=kv.device) if out is None else out
-        ro = _rows(o, "out", (n_head, kv.head_dim), kv.device)
-        if o.shape[0] != rows:
-            raise ValueError("out and q must have the same rows")
-        lse = torch.empty((rows, n_head), dtype=torch.float32, device=kv.device) if return_lse else None
-        batch._c.n_rows = rows
-        ws = workspace
-        if ws is None:
-            key = (kv._shape, n_head)
-            need = batch._space.get(key)
-            if need is None:
-                need = batch._space[key] = paged_attention_workspace(kv, batch, n_head)
-            ws = torch.empty(need, dtype=torch.uint8, device=kv.device)
-        elif ws.dtype != torch.uint8 or ws.device != kv.device or not ws.is_contiguous():
+    if not _plain(kv, batch, stream):
+        with _Call(kv, batch, stream):
+            return paged_attention(kv, batch, q, out, scale, causal, return_lse, workspace)
+    dev, hd = kv.device, kv.head_dim
+    rq = _rows(q, "q", None, hd, None, dev)
+    shape = q.shape
+    rows, n_head = shape[0], shape[1]
+    if out is None:
+        out = _t.empty(shape, dtype=q.dtype, device=dev)
+    ro = _rows(out, "out", n_head, hd, rows, dev)
+    lse = _t.empty((rows, n_head), dtype=_t.float32, device=dev) if return_lse else None
+    batch._c.n_rows = rows
+    if workspace is None:
+        key = (kv.n_kv_head, hd, n_head)
+        need = batch._space.get(key)
+        if need is None:
+            need = batch._space[key] = paged_attention_workspace(kv, batch, n_head)
+        workspace = _t.empty(need, dtype=_t.uint8, device=dev)
+    else:
+        if workspace.dtype != _t.uint8 or workspace.device != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 tensor on the pool's device")
-        _check(_lib().qwen2_paged_attention(kv._at, batch._at, n_head, ctypes.addressof(rq), ctypes.addressof(ro),
-                                            lse.data_ptr() if return_lse else None,
-                                            kv.head_dim ** -0.5 if scale is None else scale, int(causal),
-                                            ws.data_ptr(), ws.numel(), st))
-        return (o, lse) if return_lse else o
-    return _on_stream(kv, batch, stream, call)
+        need = workspace.numel()
+    rc = _lib().qwen2_paged_attention(kv._at, batch._at, n_head, ctypes.addressof(rq), ctypes.addressof(ro),
+                                      lse.data_ptr() if return_lse else None,
+                                      hd ** -0.5 if scale is None else scale, int(causal), workspace.data_ptr(), need,
+                                      _raw_stream(kv._index))
+    if rc:
+        _check(rc)
+    return (out, lse) if return_lse else out
 
 
 def paged_attention_workspace(kv: PagedKV, batch: PagedBatch, n_head: int) -> int:
     """Workspace bytes of paged_attention for these shapes."""
-    import torch
-    with torch.cuda.device(kv.device):
+    with _t.cuda.device(kv.device):
         need = _lib().qwen2_paged_attention_workspace(kv._at, batch._at, n_head)
     if need < 0:
         from . import QWEN2_E_ARG, Qwen2Error
