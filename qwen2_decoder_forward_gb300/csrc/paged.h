@@ -44,8 +44,8 @@ int tc_tile_rows(int group);
 // Tensor maps of a call; false where the strides do not allow them.
 bool tc_encode(TcMaps& m, const Pool& kv, const AttnCall& c, const Rows& q, int n_rows);
 // chained: launched right behind the few-rows kernel, which it may overlap.
-cudaError_t enqueue_attention_tc(const TcMaps& m, const AttnArgs& a, int head_dim, bool bf16, int n_sm, bool chained,
-                                 cudaStream_t st);
+cudaError_t enqueue_attention_tc(const TcMaps& m, const AttnArgs& a, int format, int head_dim, bool bf16, int n_sm,
+                                 bool chained, cudaStream_t st);
 
 }  // namespace paged
 }  // namespace qwen2

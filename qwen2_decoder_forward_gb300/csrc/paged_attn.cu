@@ -741,9 +741,9 @@ Plan plan_of(const Batch& b, const Pool& kv, int n_head, bool tensor) {
     if (b.n_seq == 1) return {0, 0, true};
     return {16, 16, true};
 }
-bool tensor_kernel(const Pool& kv, int n_head, int format, float scale) {
+bool tensor_kernel(float scale) {
     // Masked scores are -inf before the scale: it has to be positive there.
-    return (format == QWEN2_KV_F16 || format == QWEN2_KV_BF16) && scale > 0.f && n_head / kv.n_kv <= 128;
+    return scale > 0.f;
 }
 
 }  // namespace
@@ -769,7 +769,7 @@ cudaError_t enqueue_attention(const Pool& kv, const Batch& b, const AttnCall& c,
     a.scale_log2 = c.scale * 1.4426950408889634f;
     const bool bf16 = c.dtype == QWEN2_DTYPE_BF16;
     TcMaps maps;
-    Plan plan = plan_of(b, kv, c.n_head, tensor_kernel(kv, c.n_head, c.format, c.scale));
+    Plan plan = plan_of(b, kv, c.n_head, tensor_kernel(c.scale));
     if (plan.tc && !tc_encode(maps, kv, c, q, b.n_rows)) plan = plan_of(b, kv, c.n_head, false);
     JoinArgs j{};
     j.out = out;
@@ -795,7 +795,7 @@ cudaError_t enqueue_attention(const Pool& kv, const Batch& b, const AttnCall& c,
         a.rows_lo = plan.tile ? plan.few : 0;
         a.rows_hi = 0x7fffffff;
         a.parts = carve_parts(ws, n_sm, a.tile);
-        e = enqueue_attention_tc(maps, a, c.head_dim, bf16, n_sm, plan.tile != 0, st);
+        e = enqueue_attention_tc(maps, a, c.format, c.head_dim, bf16, n_sm, plan.tile != 0, st);
         if (e != cudaSuccess) return e;
         j.parts[1] = a.parts;
         j.n_cta[1] = n_sm;

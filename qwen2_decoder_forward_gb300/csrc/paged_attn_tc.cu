@@ -1,5 +1,5 @@
 // Attention over the paged cache for chunks and prompts: the products on
-// tcgen05, K, V and the queries by TMA.  16-bit pages.
+// tcgen05, the queries and 16-bit pages by TMA, 8-bit pages through registers.
 //
 //   o_i = sum_j w_ij v_j / sum_j w_ij,   w_ij = 2^(s_ij - m_i),
 //   s_ij = scale log2(e) q_i . k_j,
@@ -26,10 +26,17 @@
 // its own for head_dim 64, over its own S for head_dim 128, where S of the
 // next unit is issued once P V has completed.
 //
+// 8-bit pages: four more warps (12-15) read the codes, widen them to exact
+// 16-bit values (of the queries' type) and store the swizzled tiles that TMA
+// would have written.  The scales stay out of the products: k's multiplies the
+// scores, v's the probabilities, relative to G, the largest v scale so far
+// rounded up to a power of two, which O carries like the reference m.
+//
 // V is the [position][dim] tile as it lies in the pages: an MN-major B
 // operand, so nothing is transposed.  Positions of the last unit that are no
 // keys are zeroed in V (0 * NaN) and masked in S.
 #include <cuda.h>
+#include <cuda_fp8.h>
 
 #include "paged.cuh"
 #include "paged.h"
@@ -44,11 +51,20 @@ namespace {
 using namespace sm100;
 
 constexpr int kUnit = 128;                 // positions per unit
-constexpr int kThreads = 384;
-// Registers per thread: the softmax warps hold a row of S each.  Launched with
-// 168 (64,512 in all): 2 * 128 * 200 + 128 * 104 = 64,512.
-constexpr int kSoftmaxRegs = 200, kOtherRegs = 104;
-constexpr int kMaxStages = 12;
+enum Kind { kSame16, kInt8, kE4m3 };
+// Registers per thread (setmaxnreg): a softmax thread holds a row of S.
+// 16-bit pages: 384 threads launched with 168 (64,512 in all),
+// 2 * 128 * 200 + 128 * 104 = 64,512.  8-bit pages: 512 threads launched with
+// 128 (65,536), 2 * 128 * 184 + 2 * 128 * 72 = 65,536.
+template <Kind K>
+struct Split {
+    static constexpr int kThreads = K == kSame16 ? 384 : 512;
+    static constexpr int kSoftmax = K == kSame16 ? 200 : 184;
+    static constexpr int kOther = K == kSame16 ? 104 : 72;
+};
+constexpr int kFeeders = 4;                // warps that widen 8-bit codes
+constexpr int kScaleUnits = 4;             // units whose scales are kept (8-bit pages)
+constexpr int kMaxStages = 12, kMaxStages8 = 6;
 constexpr int kHalfBytes = 128 * 128;      // 128 rows of 64 16-bit elements
 constexpr uint32_t kTmemCols = 512;
 constexpr float kSlack = 8.f;              // log2 of the growth that is left in the weights
@@ -57,11 +73,12 @@ struct TcSmem {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], tail, drain;
     unsigned bad[8];                       // per unit (mod 8): its positions in bad pages, 16 per bit
+    int g[kScaleUnits];                    // 8-bit pages, per unit (mod 4): log2 of G
     uint32_t tmem_slot;
     int abort;
 };
 constexpr int kHead = 1024;                // TcSmem, in front of the 1024-byte aligned tiles
-static_assert(sizeof(TcSmem) <= kHead, "");
+static_assert(sizeof(TcSmem) <= kHead - 64, "");      // the last 64 bytes: the feeders' reduction
 
 struct TcArgs {
     AttnArgs a;
@@ -215,26 +232,96 @@ __device__ __forceinline__ void put_row32(char* dst, const uint32_t (&o)[32], fl
     }
 }
 
-template <int HD, bool BF16>
-__global__ void __launch_bounds__(kThreads, 1)
+// 16 codes as 16-bit values, in order; exact.
+template <Kind K, bool BF16>
+__device__ __forceinline__ void widen16(const uint4& raw, uint32_t (&o)[8]) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if constexpr (K == kInt8 && !BF16) {
+                // 1024 + (c + 128), minus 1152.
+                const uint32_t h = __byte_perm(w[i] ^ 0x80808080u, 0x64646464u, j ? 0x4342 : 0x4140);
+                const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x6480)));
+                o[2 * i + j] = *reinterpret_cast<const uint32_t*>(&v);
+            } else if constexpr (K == kInt8) {
+                // c = (128 + its low 7 bits) - (128, or 256 if negative).
+                const uint32_t h = __byte_perm(w[i], 0x43434343u, j ? 0x4342 : 0x4140);
+                const uint32_t x = h & 0xff7fff7fu, y = h & 0xff80ff80u;
+                const __nv_bfloat162 v =
+                    __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+                o[2 * i + j] = *reinterpret_cast<const uint32_t*>(&v);
+            } else {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[i] >> (16 * j)), __NV_E4M3);
+                if constexpr (!BF16) {
+                    o[2 * i + j] = (uint32_t)h.x | (uint32_t)h.y << 16;
+                } else {
+                    const float2 f = __half22float2(__half2(h));
+                    o[2 * i + j] = pack2<true>(f.x, f.y);
+                }
+            }
+        }
+}
+
+// The power of two at or above v, as an exponent in [-100, 100].
+__device__ __forceinline__ int ceil_log2(float v) {
+    const int b = __float_as_int(v);
+    const int e = ((b >> 23) & 255) - 127 + ((b & 0x7fffff) != 0);
+    return min(max(e, -100), 100);
+}
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// Barrier of the four feeding warps that tells all of them whether every one
+// got through its wait: they go on, or stop, together.
+__device__ __forceinline__ bool feeders_agree(bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)ok)
+        : "memory");
+    return all != 0;
+}
+
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+
+template <int HD, bool BF16, Kind K>
+__global__ void __launch_bounds__(Split<K>::kThreads, 1)
     k_paged_attn_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcArgs args) {
     using T = Tmem<HD>;
     constexpr int kHalves = HD / 64;
     constexpr int kTileBytes = kHalves * kHalfBytes;
+    constexpr bool k8 = K != kSame16;
     const AttnArgs& a = args.a;
     extern __shared__ unsigned char tc_smem_raw[];
     const uint32_t pad = (1024u - (smem_addr(tc_smem_raw) & 1023u)) & 1023u;
     TcSmem& sm = *reinterpret_cast<TcSmem*>(tc_smem_raw + pad);
     const uint32_t q_tiles = smem_addr(&sm) + kHead;                 // A, B
     const uint32_t ring = q_tiles + 2 * kTileBytes;
-    long long* prefix = reinterpret_cast<long long*>(tc_smem_raw + pad + kHead + (2 + args.stages) * kTileBytes);
+    const uint32_t scales = ring + args.stages * kTileBytes;         // 8-bit: [kScaleUnits][k, v / G][kUnit] f32
+    long long* prefix = reinterpret_cast<long long*>(tc_smem_raw + pad + kHead + (2 + args.stages) * kTileBytes +
+                                                     (k8 ? kScaleUnits * 2 * kUnit * 4 : 0));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_launch_dependents();
     if (tid == 0) {
         for (int i = 0; i < args.stages; ++i) {
-            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.full[i], k8 ? kFeeders : 1);
             mbar_init(&sm.empty[i], 1);
         }
         mbar_init(&sm.q_full, 1);
@@ -252,8 +339,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8) tmem_alloc(&sm.tmem_slot, kTmemCols);
     if (warp == 9 && lane == 0) {
         tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
+        if constexpr (!k8) {
+            tma_prefetch_desc(&tm_k);
+            tma_prefetch_desc(&tm_v);
+        }
     }
     const WorkList work = build_work<kUnit>(a, prefix, args.min_units);
     tc_fence_before();
@@ -266,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (left > 0) {
         Tile t = find_tile<kUnit>(a, work, work.begin, left);
         if (warp < 8) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Split<K>::kSoftmax));
             // ---- softmax of half x --------------------------------------------------
             const int x = warp >> 2, rl = 32 * (warp & 3) + lane;
             const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -283,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int lim = live ? min(row_limit(a, t.q, i), t.keys - 1) : t.keys - 1;
                     const int sure = min(row_limit(a, t.q, packed0 + x * args.sub), t.keys - 1);
                     float m = -INFINITY, l0 = 0.f, l1 = 0.f;
+                    int g = -100;          // log2 of G
                     for (int u = 0; u < t.n; ++u, ++n_s) {
                         const int key0 = (t.u0 + u) * kUnit;
                         ok = __all_sync(0xffffffffu, wait(&sm.s_full[x], n_s & 1, sm, a.b.guard));
@@ -295,6 +385,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld_wait();
 #pragma unroll
                         for (int c = 0; c < 4; ++c) pin32(s[c]);
+                        const uint32_t at = scales + ((unit + u) % kScaleUnits) * (2 * kUnit * 4);
+                        if constexpr (k8) {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4) {
+                                    const float4 ks = lds4(at + 4 * (32 * c + e));
+                                    float y[4] = {__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]),
+                                                  __uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3])};
+                                    mul2(y[0], y[1], ks.x, ks.y);
+                                    mul2(y[2], y[3], ks.z, ks.w);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) s[c][e + i] = __float_as_uint(y[i]);
+                                }
+                        }
                         if (key0 + kUnit - 1 > sure || bad) {
 #pragma unroll
                             for (int c = 0; c < 4; ++c)
@@ -318,7 +423,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             l0 *= corr;
                             l1 *= corr;
                         }
-                        if (u > 0 && __any_sync(0xffffffffu, move)) {
+                        bool scale_o = __any_sync(0xffffffffu, move);
+                        if constexpr (k8) {
+                            const int ng = sm.g[(unit + u) % kScaleUnits];
+                            corr *= pow2i(max(g - ng, -126));
+                            scale_o = scale_o || ng != g;
+                            g = ng;
+                        }
+                        if (u > 0 && scale_o) {
                             ok = __all_sync(0xffffffffu, wait(&sm.o_full[x], (n_s - 1) & 1, sm, a.b.guard));
                             if (!ok) break;
                             tc_fence_after();
@@ -337,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             uint32_t p[32];
+                            [[maybe_unused]] float4 vs;
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
                                 float y = __uint_as_float(s[2 * c + e / 16][2 * e % 32]);
@@ -345,6 +458,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 y = ex2(y);
                                 z = ex2(z);
                                 add2(l0, l1, y, z);
+                                if constexpr (k8) {
+                                    if (e % 2 == 0) vs = lds4(at + 4 * kUnit + 4 * (64 * c + 2 * e));
+                                    mul2(y, z, e % 2 ? vs.z : vs.x, e % 2 ? vs.w : vs.y);
+                                }
                                 p[e] = pack2<BF16>(y, z);
                             }
                             tmem_st32(t_p + 32 * c, p);
@@ -358,11 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = __all_sync(0xffffffffu, wait(&sm.o_full[x], (n_s - 1) & 1, sm, a.b.guard));
                     if (!ok) break;
                     tc_fence_after();
-                    const float l = l0 + l1;
+                    const float l = l0 + l1, unit_g = k8 ? pow2i(g) : 1.f;
                     const bool begins = t.u0 == 0, ends = t.u0 + t.n >= t.units;
                     const int slot = slot0 + (begins ? 1 : 0), r = x * args.sub + rl;
                     if (begins && ends) {
-                        const float inv = l == 0.f ? 0.f : 1.f / l;
+                        const float inv = l == 0.f ? 0.f : unit_g / l;
                         const int row = t.q.q0 + i / a.group, qh = t.head * a.group + i % a.group;
                         char* dst = a.out.data + (long long)row * a.out.row_bytes + (long long)qh * a.out.head_bytes;
 #pragma unroll
@@ -387,8 +504,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (live)
 #pragma unroll
                                 for (int e = 0; e < 8; ++e)
-                                    reinterpret_cast<uint4*>(po + 32 * c)[e] =
-                                        make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                                    reinterpret_cast<float4*>(po + 32 * c)[e] = make_float4(
+                                        __uint_as_float(o[4 * e]) * unit_g, __uint_as_float(o[4 * e + 1]) * unit_g,
+                                        __uint_as_float(o[4 * e + 2]) * unit_g, __uint_as_float(o[4 * e + 3]) * unit_g);
                         }
                         if (live) {
                             a.parts.ml[(long long)slot * 2 * a.parts.rows + r] = m;
@@ -414,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 next_tile<kUnit>(a, work, t, left);
             }
         } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<K>::kOther));
         }
         if (warp == 8) {
             // ---- products -------------------------------------------------------------
@@ -488,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         } else if (warp == 9) {
-            // ---- feed -------------------------------------------------------------------
+            // ---- feed: queries, and 16-bit pages ------------------------------------------
             const int page_rows = 1 << a.kv.page_shift, box = min(page_rows, kUnit), boxes = kUnit / box;
             const int p = lane / kHalves, h = lane % kHalves;
             unsigned ent = 0, seg = 0, unit = 0, n_tail = 0;
@@ -506,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
                 ++seg;
-                for (int u = 0; u < t.n && ok; ++u, ++unit) {
+                for (int u = 0; !k8 && u < t.n && ok; ++u, ++unit) {
                     const int key0 = (t.u0 + u) * kUnit, key = key0 + p * box;
                     int page = -1;
                     bool is_bad = false;
@@ -571,6 +689,108 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (seg) mbar_wait(&sm.q_full, (seg - 1) & 1, kWaitNs);
             }
             __syncwarp();
+        } else if (k8 && warp >= 12) {
+            // ---- feed: 8-bit pages ------------------------------------------------------
+            // Thread e takes 16-byte piece e % 4 of row e / 4 (+ 32 rows a step) of
+            // each 64-dim half: two adjacent rows' pieces fill all banks.
+            const int e0 = tid - 384, piece = e0 & 3, row0 = e0 >> 2;
+            constexpr int kPieces = 4 * kHalves;        // per thread and tile
+            unsigned ent = 0, unit = 0;
+            bool ok = true, stop = false;
+            while (!stop) {
+                int g = -100;
+                for (int u = 0; u < t.n; ++u, ++unit) {
+                    const int key0 = (t.u0 + u) * kUnit;
+                    // Lane l holds the page of positions 16 (l % 8) .. of the unit.
+                    const int key_l = key0 + 16 * (lane & 7);
+                    int page_l = -1;
+                    bool is_bad = false;
+                    if (key_l < t.keys) {
+                        page_l = __ldg(a.b.pages + (long long)t.s * a.b.pages_stride + (key_l >> a.kv.page_shift));
+                        if ((unsigned)page_l >= (unsigned)a.kv.n_pages) {
+                            is_bad = true;
+                            page_l = -1;
+                            raise_guard(a.b.guard, QWEN2_GUARD_PAGE);
+                        }
+                    }
+                    const unsigned bad = __ballot_sync(0xffffffffu, is_bad) & 0xffu;
+                    // This thread's rows: row0 + 32 j, j = 0 .. 3.
+                    long long src[4];
+                    bool in[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = row0 + 32 * j, pg = __shfl_sync(0xffffffffu, page_l, r >> 4);
+                        in[j] = pg >= 0 && key0 + r < t.keys;
+                        src[j] = in[j] ? (long long)pg * a.kv.page_bytes +
+                                             (long long)((key0 + r) & ((1 << a.kv.page_shift) - 1)) * a.kv.token_bytes +
+                                             (long long)t.head * a.kv.head_bytes + 16 * piece
+                                       : 0;
+                    }
+                    // Position e0's scales.
+                    const int pg_s = __shfl_sync(0xffffffffu, page_l, (e0 >> 4) & 7);
+                    float ks = 0.f, vs = 0.f;
+                    if (pg_s >= 0 && key0 + e0 < t.keys) {
+                        const long long i = (((long long)pg_s * a.kv.n_kv + t.head) << a.kv.page_shift) +
+                                            ((key0 + e0) & ((1 << a.kv.page_shift) - 1));
+                        ks = __ldg(a.kv.k_scale + i);
+                        vs = __ldg(a.kv.v_scale + i);
+                    }
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const char* base = kv ? a.kv.v : a.kv.k;
+                        uint4 raw[kPieces];
+#pragma unroll
+                        for (int i = 0; i < kPieces; ++i)
+                            raw[i] = in[i & 3] ? __ldg(reinterpret_cast<const uint4*>(base + src[i & 3] + 64 * (i >> 2)))
+                                               : make_uint4(0, 0, 0, 0);
+                        const unsigned st = ent % (unsigned)args.stages, round = ent / (unsigned)args.stages;
+                        if (round && ok) ok = __all_sync(0xffffffffu, wait(&sm.empty[st], (round - 1) & 1, sm, a.b.guard));
+                        if (kv == 0) {
+                            // The slot of this unit's scales is free: with at most 6 stages the V tile stored last took
+                            // the place of one whose P V had completed, of the unit kScaleUnits back or a later one.
+                            const unsigned slot = unit % kScaleUnits;
+                            // The largest v scale of the unit, over the four warps.
+                            float top = warp_max(vs);
+                            float* red = reinterpret_cast<float*>(&sm) + (kHead - 64) / 4 + 4 * (unit & 1);
+                            if (lane == 0) red[warp & 3] = top;
+                            stop = !feeders_agree(ok);
+                            if (stop) break;
+                            top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+                            g = max(g, ceil_log2(top));
+                            const uint32_t at = scales + slot * (2 * kUnit * 4) + 4 * e0;
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(ks) : "memory");
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * kUnit), "f"(vs * pow2i(-g)) : "memory");
+                            if (e0 == 0) {
+                                sm.g[slot] = g;
+                                sm.bad[unit & 7] = (bad & 0xffu);
+                            }
+                        }
+                        if (!ok) break;     // the others learn of it at the next unit's barrier
+                        const uint32_t tile = ring + st * kTileBytes;
+#pragma unroll
+                        for (int i = 0; i < kPieces; ++i) {
+                            uint32_t o[8];
+                            widen16<K, BF16>(raw[i], o);
+                            const int r = row0 + 32 * (i & 3);
+                            const uint32_t at = tile + (i >> 2) * kHalfBytes + r * 128;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                                 at + (((2 * piece + j) ^ (r & 7)) << 4)),
+                                             "r"(o[4 * j]), "r"(o[4 * j + 1]), "r"(o[4 * j + 2]), "r"(o[4 * j + 3])
+                                             : "memory");
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.full[st]);
+                        ++ent;
+                    }
+                    if (stop) break;
+                }
+                left -= t.n;
+                if (left <= 0) break;
+                next_tile<kUnit>(a, work, t, left);
+            }
         }
     }
     if (tid == 0) {
@@ -635,19 +855,29 @@ bool encode_q(CUtensorMap* m, const Rows& q, int n_rows, int n_head, int group, 
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int HD, bool BF16>
+template <int HD, bool BF16, Kind K>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, TcArgs& args, int n_sm,
                    bool chained, cudaStream_t st) {
-    constexpr int kTileBytes = HD / 64 * kHalfBytes;
-    auto kern = k_paged_attn_tc<HD, BF16>;
+    constexpr int kTileBytes = HD / 64 * kHalfBytes, kThreads = Split<K>::kThreads;
+    auto kern = k_paged_attn_tc<HD, BF16, K>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
-    const int prefix = 8 * (args.a.b.n_seq + 1), room = 227 * 1024 - 1024 - kHead - prefix - 2 * kTileBytes;
-    args.stages = min(kMaxStages, room / kTileBytes);
-    const size_t smem = 1024 + kHead + (size_t)(2 + args.stages) * kTileBytes + prefix;
+    const int rest = 8 * (args.a.b.n_seq + 1) + (K == kSame16 ? 0 : kScaleUnits * 2 * kUnit * 4);
+    const int room = 227 * 1024 - 1024 - kHead - rest - 2 * kTileBytes;
+    args.stages = min(K == kSame16 ? kMaxStages : kMaxStages8, room / kTileBytes);
+    const size_t smem = 1024 + kHead + (size_t)(2 + args.stages) * kTileBytes + rest;
     if (chained) return launch_pdl(kern, dim3(n_sm), dim3(kThreads), smem, st, q, k, v, args);
     kern<<<n_sm, kThreads, smem, st>>>(q, k, v, args);
     return cudaGetLastError();
+}
+
+template <Kind K>
+cudaError_t launch_hd(const TcMaps& m, TcArgs& args, int head_dim, bool bf16, int n_sm, bool chained, cudaStream_t st) {
+    if (head_dim == 64)
+        return bf16 ? launch<64, true, K>(m.q, m.k, m.v, args, n_sm, chained, st)
+                    : launch<64, false, K>(m.q, m.k, m.v, args, n_sm, chained, st);
+    return bf16 ? launch<128, true, K>(m.q, m.k, m.v, args, n_sm, chained, st)
+                : launch<128, false, K>(m.q, m.k, m.v, args, n_sm, chained, st);
 }
 
 }  // namespace
@@ -658,24 +888,26 @@ bool tc_encode(TcMaps& m, const Pool& kv, const AttnCall& c, const Rows& q, int 
     const bool bf16 = c.dtype == QWEN2_DTYPE_BF16;
     const int group = c.n_head / kv.n_kv;
     int rank_v[3];
+    if (!encode_q(&m.q, q, n_rows, c.n_head, group, 128 / group, c.head_dim, bf16)) return false;
+    if (c.format == QWEN2_KV_INT8 || c.format == QWEN2_KV_E4M3) {
+        m.k = m.v = m.q;      // not used
+        return true;
+    }
     return encode_pool(&m.k, kv.k, kv, c.head_dim, bf16, m.kv_rank) &&
-           encode_pool(&m.v, kv.v, kv, c.head_dim, bf16, rank_v) &&
-           encode_q(&m.q, q, n_rows, c.n_head, group, 128 / group, c.head_dim, bf16);
+           encode_pool(&m.v, kv.v, kv, c.head_dim, bf16, rank_v);
 }
 
-cudaError_t enqueue_attention_tc(const TcMaps& m, const AttnArgs& a, int head_dim, bool bf16, int n_sm, bool chained,
-                                 cudaStream_t st) {
+cudaError_t enqueue_attention_tc(const TcMaps& m, const AttnArgs& a, int format, int head_dim, bool bf16, int n_sm,
+                                 bool chained, cudaStream_t st) {
     TcArgs args{};
     args.a = a;
     args.sub = a.tile / 2;
     args.sub_rows = args.sub / a.group;
     for (int i = 0; i < 3; ++i) args.kv_rank[i] = m.kv_rank[i];
     args.min_units = 2;
-    if (head_dim == 64)
-        return bf16 ? launch<64, true>(m.q, m.k, m.v, args, n_sm, chained, st)
-                    : launch<64, false>(m.q, m.k, m.v, args, n_sm, chained, st);
-    return bf16 ? launch<128, true>(m.q, m.k, m.v, args, n_sm, chained, st)
-                : launch<128, false>(m.q, m.k, m.v, args, n_sm, chained, st);
+    if (format == QWEN2_KV_INT8) return launch_hd<kInt8>(m, args, head_dim, bf16, n_sm, chained, st);
+    if (format == QWEN2_KV_E4M3) return launch_hd<kE4m3>(m, args, head_dim, bf16, n_sm, chained, st);
+    return launch_hd<kSame16>(m, args, head_dim, bf16, n_sm, chained, st);
 }
 
 }  // namespace paged

@@ -124,7 +124,8 @@ class Case:
 
 def check_attention(c, q, held, o, lse, scale, causal, out_fill):
     """|o - exact| by arithmetic: with A = sum w |v| / sum w,
-      * each probability is rounded to the product's 16-bit type: A u_P;
+      * each probability is rounded to the product's 16-bit type, q's own (f16 over 8-bit pages where a sequence
+        has at most 32 rows of a kv head's group): A u_P;
       * a score's error d (f32 products of hd terms, its scaling and the
         exponential's 2^-22) turns into a factor 1 +- 2 d on weights: 4 d A
         over numerator and denominator;
@@ -132,7 +133,8 @@ def check_attention(c, q, held, o, lse, scale, causal, out_fill):
         a subnormal step (f16: 2^-25) times |v| (8-bit: times the largest
         scale, rounded up to a power of two, times the code);
       * the output's own rounding u_o |o|."""
-    p_type = torch.float16 if c.quant or q.dtype == torch.float16 else torch.bfloat16
+    few = c.batch.max_q * (c.nh // c.nkv) <= 32
+    p_type = torch.float16 if q.dtype == torch.float16 or (c.quant and few) else torch.bfloat16
     sub = 2.0 ** -25 if p_type == torch.float16 else 2.0 ** -134
     for s, (n, kv) in enumerate(c.seqs):
         if n == 0:
