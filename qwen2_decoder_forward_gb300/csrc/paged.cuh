@@ -55,13 +55,15 @@ __device__ __forceinline__ Seq load_seq(const Batch& b, int page_shift, int s) {
 // The query rows of one sequence and kv head are the pairs (row, query head of
 // the group), row-major: packed row i = row * group + head.  They are cut into
 // tiles of `tile` packed rows, and each tile's keys into units of kKeys
-// positions; a tile without keys is one unit.  The units of all tiles, ordered
-// (sequence, kv head, tile, unit), form one list, of which CTA c of g takes
-// the contiguous part [W c / g, W (c + 1) / g): every CTA has the same work
-// whatever the mix of lengths, and a tile is cut at most where two CTAs'
-// parts meet.  A CTA that covers a whole tile writes its rows itself; the
-// others leave a partial (row maxima, sums, unnormalised rows) that
-// k_attn_join adds up in list order, so results do not depend on timing.
+// positions; a tile without keys is one unit.  Every tile takes kCost slots
+// for what it costs beside its units (its queries, its rows on their way out)
+// and one per unit; the slots of all tiles, ordered (sequence, kv head, tile,
+// unit), form one list, of which CTA c of g takes the contiguous c-th part:
+// every CTA has the same work whatever the mix of lengths, and a tile is cut
+// at most where two CTAs' parts meet (a cut among the kCost slots leaves the
+// tile to the later CTA).  A CTA that covers a whole tile writes its rows
+// itself; the others leave a partial (row maxima, sums, unnormalised rows)
+// that k_attn_join adds up in list order, so results do not depend on timing.
 
 // Keys that the tile of packed rows [i0, i0 + rows) sees: its last row's.
 __device__ __forceinline__ int tile_keys(const Seq& q, int group, int i0, int rows, bool causal) {
@@ -76,30 +78,30 @@ __device__ __forceinline__ int tile_units(const Seq& q, int group, int t, int ro
 }
 
 // What a CTA left in the workspace: slot 0 the part of a tile that an earlier
-// CTA began, slot 1 the beginning of a tile that goes on in the next CTA.
+// CTA began, slot 1 the beginning of a tile that goes on in the next CTAs;
+// PartInfo describes slot 1.
 struct PartInfo {
+    int n;                               // parts of the tile, this one included; 0: no open tile
     int q0, packed0, packed_end, head;   // rows of the batch from q0; packed rows [packed0, packed_end) of kv head `head`
-    int state;                           // kPartNone, or bits
     int pad[3];
 };
-constexpr int kPartNone = 0, kPartUsed = 1, kPartLast = 2;   // kPartLast: the tile ends here
 
 // The workspace of one attention kernel: g CTAs of tiles of `rows` packed rows.
 struct Parts {
-    PartInfo* info;   // [2 g]
+    PartInfo* info;   // [g]
     float* ml;        // [2 g][2][rows]: row maxima (base 2), sums
     float* o;         // [2 g][rows][hd]
     int rows;
 };
 __host__ __device__ inline long long parts_bytes(int g, int rows, int hd) {
-    const long long b = 2ll * g * (sizeof(PartInfo) + 2ll * rows * 4 + (long long)rows * hd * 4);
+    const long long b = (long long)g * (sizeof(PartInfo) + 2 * (2ll * rows * 4 + (long long)rows * hd * 4));
     return (b + 255) / 256 * 256;
 }
 inline Parts carve_parts(void* ws, int g, int rows) {
     Parts p;
     char* c = static_cast<char*>(ws);
     p.info = reinterpret_cast<PartInfo*>(c);
-    p.ml = reinterpret_cast<float*>(c + 2ll * g * sizeof(PartInfo));
+    p.ml = reinterpret_cast<float*>(c + (long long)g * sizeof(PartInfo));
     p.o = p.ml + 4ll * g * rows;
     p.rows = rows;
     return p;
@@ -124,14 +126,19 @@ struct Tile {
     int s, head, t;          // sequence, kv head, tile index
     Seq q;
     int keys, units;         // keys the tile sees, and their units
-    int u0, n;               // first unit and number of units of this CTA's part
+    long long at;            // its first slot in the list
+    int u0, n;               // first unit and number of units of this CTA's part; n <= 0: past its end
 };
 
-// Sums of the units of the first s sequences, and the CTA's share; one copy in
-// shared memory per CTA.
+// Sums of the slots of the first s sequences, and the CTA's share.
 struct WorkList {
     const long long* prefix;   // shared memory [n_seq + 1]
-    long long begin, end;      // this CTA's units
+    long long begin, end;      // this CTA's slots
+    long long each, rest;      // the first `rest` CTAs take each + 1 slots, the others `each`
+    __device__ __forceinline__ int owner(long long slot) const {
+        const long long big = rest * (each + 1);
+        return (int)(slot < big ? slot / (each + 1) : rest + (slot - big) / each);
+    }
 };
 
 __device__ __forceinline__ bool owns(const AttnArgs& a, const Seq& q) {
@@ -140,10 +147,10 @@ __device__ __forceinline__ bool owns(const AttnArgs& a, const Seq& q) {
 }
 
 // Builds the prefix sums with the whole block (at most 4096 sequences) and
-// returns this CTA's share.  min_units: a CTA gets at least that many units
-// (but the last), so that small batches are not cut finer than pays.
-template <int kKeys>
-__device__ __forceinline__ WorkList build_work(const AttnArgs& a, long long* prefix, int min_units) {
+// returns this CTA's share.  A CTA gets at least min_slots > kCost slots, so
+// that small batches are not cut finer than pays and every part has a unit.
+template <int kKeys, int kCost>
+__device__ __forceinline__ WorkList build_work(const AttnArgs& a, long long* prefix, int min_slots) {
     // A thread per sequence; one with many causal tiles (each of its own length)
     // is left to a whole warp.
     for (int s = threadIdx.x; s < a.b.n_seq; s += blockDim.x) {
@@ -153,9 +160,9 @@ __device__ __forceinline__ WorkList build_work(const AttnArgs& a, long long* pre
         long long u = 0;
         if (owns(a, q)) {
             const int tiles = (q.n * a.group + a.tile - 1) / a.tile;
-            if (!a.causal) u = (long long)tiles * tile_units<kKeys>(q, a.group, 0, a.tile, false);
+            if (!a.causal) u = (long long)tiles * (kCost + tile_units<kKeys>(q, a.group, 0, a.tile, false));
             else if (tiles <= 4)
-                for (int t = 0; t < tiles; ++t) u += tile_units<kKeys>(q, a.group, t, a.tile, true);
+                for (int t = 0; t < tiles; ++t) u += kCost + tile_units<kKeys>(q, a.group, t, a.tile, true);
             else u = -1;
         }
         prefix[s + 1] = u < 0 ? u : u * a.kv.n_kv;
@@ -166,7 +173,7 @@ __device__ __forceinline__ WorkList build_work(const AttnArgs& a, long long* pre
         const Seq q = load_seq(a.b, a.kv.page_shift, s);
         const int tiles = (q.n * a.group + a.tile - 1) / a.tile;
         long long u = 0;
-        for (int t = threadIdx.x & 31; t < tiles; t += 32) u += tile_units<kKeys>(q, a.group, t, a.tile, true);
+        for (int t = threadIdx.x & 31; t < tiles; t += 32) u += kCost + tile_units<kKeys>(q, a.group, t, a.tile, true);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
         if ((threadIdx.x & 31) == 0) prefix[s + 1] = u * a.kv.n_kv;
@@ -190,45 +197,53 @@ __device__ __forceinline__ WorkList build_work(const AttnArgs& a, long long* pre
     }
     __syncthreads();
     const long long total = prefix[a.b.n_seq];
-    const long long most = (total + min_units - 1) / min_units;
+    const long long most = total / min_slots;
     const long long g = most < (long long)gridDim.x ? (most > 0 ? most : 1) : (long long)gridDim.x;
     WorkList w;
     w.prefix = prefix;
     const long long c = blockIdx.x;
     // total / g and the remainder keep the products within 64 bits.
-    const long long each = total / g, rest = total - each * g;
-    w.begin = c < g ? each * c + (c < rest ? c : rest) : total;
-    w.end = c < g ? w.begin + each + (c < rest ? 1 : 0) : total;
+    w.each = total / g;
+    w.rest = total - w.each * g;
+    w.begin = c < g ? w.each * c + (c < w.rest ? c : w.rest) : total;
+    w.end = c < g ? w.begin + w.each + (c < w.rest ? 1 : 0) : total;
     return w;
 }
 
-// The tile that holds unit `u` of the list, with up to `left` units of it.
-// Called by whole warps.
-template <int kKeys>
-__device__ __forceinline__ Tile find_tile(const AttnArgs& a, const WorkList& w, long long u, long long left) {
-    int lo = 0, hi = a.b.n_seq;          // largest s with prefix[s] <= u and units of its own
+// The CTA's part of a tile whose `at` and `units` are set.
+template <int kCost>
+__device__ __forceinline__ void set_part(const WorkList& w, Tile& t) {
+    t.u0 = (int)max(0ll, w.begin - t.at - kCost);
+    t.n = (int)min((long long)t.units, max(0ll, w.end - t.at - kCost)) - t.u0;
+}
+
+// The tile that holds the CTA's first slot.  Called by whole warps, for a part
+// that is not empty.
+template <int kKeys, int kCost>
+__device__ __forceinline__ Tile find_tile(const AttnArgs& a, const WorkList& w) {
+    int lo = 0, hi = a.b.n_seq;          // largest s with prefix[s] <= begin: it has slots of its own
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (w.prefix[mid] <= u) lo = mid;
+        if (w.prefix[mid] <= w.begin) lo = mid;
         else hi = mid;
     }
     Tile t;
     t.s = lo;
     t.q = load_seq(a.b, a.kv.page_shift, lo);
     const long long per_head = (w.prefix[lo + 1] - w.prefix[lo]) / a.kv.n_kv;
-    long long r = u - w.prefix[lo];
+    long long r = w.begin - w.prefix[lo];
     t.head = (int)(r / per_head);
     r -= t.head * per_head;
     const int tiles = (t.q.n * a.group + a.tile - 1) / a.tile;
     if (!a.causal) {
-        t.units = tile_units<kKeys>(t.q, a.group, 0, a.tile, false);
-        t.t = (int)(r / t.units);
-        r -= (long long)t.t * t.units;
+        const int slots = kCost + tile_units<kKeys>(t.q, a.group, 0, a.tile, false);
+        t.t = (int)(r / slots);
+        r -= (long long)t.t * slots;
     } else {
-        // 32 tiles at a time: the first one whose units reach past r.
+        // 32 tiles at a time: the first one whose slots reach past r.
         const int lane = threadIdx.x & 31;
         for (int t0 = 0;; t0 += 32) {
-            const int own = t0 + lane < tiles ? tile_units<kKeys>(t.q, a.group, t0 + lane, a.tile, true) : 0;
+            const int own = t0 + lane < tiles ? kCost + tile_units<kKeys>(t.q, a.group, t0 + lane, a.tile, true) : 0;
             long long sum = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -238,7 +253,6 @@ __device__ __forceinline__ Tile find_tile(const AttnArgs& a, const WorkList& w, 
             const unsigned hit = __ballot_sync(0xffffffffu, sum > r);
             const int at = hit ? __ffs(hit) - 1 : 31;
             const long long before = __shfl_sync(0xffffffffu, sum - own, at);
-            t.units = __shfl_sync(0xffffffffu, own, at);
             t.t = t0 + at;
             if (hit || t0 + 32 >= tiles) {
                 r -= before;
@@ -249,30 +263,56 @@ __device__ __forceinline__ Tile find_tile(const AttnArgs& a, const WorkList& w, 
         t.t = min(t.t, tiles - 1);
     }
     t.keys = tile_keys(t.q, a.group, t.t * a.tile, a.tile, a.causal);
-    t.units = max(1, t.units);
-    t.u0 = (int)r;
-    t.n = max(1, (int)min((long long)(t.units - t.u0), left));
+    t.units = max(1, (t.keys + kKeys - 1) / kKeys);
+    t.at = w.begin - r;
+    set_part<kCost>(w, t);
     return t;
 }
 
-// The tile after `t` in the list.
-template <int kKeys>
-__device__ __forceinline__ void next_tile(const AttnArgs& a, const WorkList& w, Tile& t, long long left) {
+// The tile after `t` in the list; its n is <= 0 past the CTA's part.
+template <int kKeys, int kCost>
+__device__ __forceinline__ void next_tile(const AttnArgs& a, const WorkList& w, Tile& t) {
+    t.at += kCost + t.units;
+    t.n = 0;
+    if (t.at + kCost >= w.end) return;
     const int tiles = (t.q.n * a.group + a.tile - 1) / a.tile;
-    if (++t.t == tiles) {
+    if (++t.t >= tiles) {
         t.t = 0;
         if (++t.head == a.kv.n_kv) {
             t.head = 0;
             do ++t.s;
             while (t.s + 1 < a.b.n_seq && w.prefix[t.s + 1] == w.prefix[t.s]);
-            t.s = min(t.s, a.b.n_seq - 1);
+            if (t.s >= a.b.n_seq) return;
             t.q = load_seq(a.b, a.kv.page_shift, t.s);
         }
     }
     t.keys = tile_keys(t.q, a.group, t.t * a.tile, a.tile, a.causal);
     t.units = max(1, (t.keys + kKeys - 1) / kKeys);
-    t.u0 = 0;
-    t.n = (int)min((long long)t.units, left);
+    set_part<kCost>(w, t);
+}
+
+// How a CTA's part of a tile lies in it, and where its partial goes.
+struct PartPlace {
+    bool whole, begins;
+    int slot;
+};
+__device__ __forceinline__ PartPlace part_place(const Tile& t) {
+    PartPlace p;
+    p.begins = t.u0 == 0;
+    p.whole = p.begins && t.n >= t.units;
+    p.slot = 2 * blockIdx.x + (p.begins ? 1 : 0);
+    return p;
+}
+// By one thread, for a tile that begins here and goes on in the next CTA.
+template <int kCost>
+__device__ __forceinline__ void note_open(const AttnArgs& a, const WorkList& w, const Tile& t) {
+    PartInfo pi;
+    pi.n = w.owner(t.at + kCost + t.units - 1) - (int)blockIdx.x + 1;
+    pi.q0 = t.q.q0;
+    pi.packed0 = t.t * a.tile;
+    pi.packed_end = min(pi.packed0 + a.tile, t.q.n * a.group);
+    pi.head = t.head;
+    a.parts.info[blockIdx.x] = pi;
 }
 
 // Last position packed row i of a sequence sees.

@@ -43,6 +43,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 64;      // positions per unit
 constexpr int kStep = 16;      // positions per warp and unit
+constexpr int kCost = 1;       // slots of a tile beside its units (paged.cuh)
 
 enum Kind { kSame16, kInt8, kE4m3 };
 
@@ -154,16 +155,11 @@ __device__ __forceinline__ int ceil_log2(float v) {
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
-__device__ __forceinline__ void store_part_none(const Parts& p, int slot) {
-    if (threadIdx.x == 0) p.info[slot].state = kPartNone;
-}
-
 // The copies of one warp step: cursor over the CTA's units, `ahead` steps
 // before the products.
 struct Feed {
     Tile t;
     int i;                 // unit within the tile's part
-    long long left;        // units of the CTA not yet handed out, this tile's included
 };
 
 template <int HD, Kind K, bool BF16, int MT>
@@ -181,18 +177,16 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t4 = lane & 3;
-    const WorkList work = build_work<kUnit>(a, prefix, 1);
-    const int slot0 = 2 * blockIdx.x;
-    bool wrote0 = false, wrote1 = false;
-    long long left = work.end - work.begin;
-    if (left > 0) {
+    const WorkList work = build_work<kUnit, kCost>(a, prefix, kCost + 1);
+    bool open = false;
+    if (work.begin < work.end) {
         const uint32_t ring = (uint32_t)__cvta_generic_to_shared(rings + warp * S::kRing);
-        Tile t = find_tile<kUnit>(a, work, work.begin, left);
-        Feed f{t, 0, left};
+        Tile t = find_tile<kUnit, kCost>(a, work);
+        Feed f{t, 0};
         int f_page = -1;
         // Page of the feed's current step; -1 if it has no keys, -2 if its id is bad.
         auto look_up = [&]() -> int {
-            if (f.left <= 0) return -1;
+            if (f.t.n <= 0) return -1;
             const int key0 = (f.t.u0 + f.i) * kUnit + warp * kStep;
             if (key0 >= f.t.keys) return -1;
             const int p = __ldg(a.b.pages + (long long)f.t.s * a.b.pages_stride + (key0 >> a.kv.page_shift));
@@ -231,12 +225,9 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
                 if (lane == 0) raise_guard(a.b.guard, QWEN2_GUARD_PAGE);
             }
             cp_commit();
-            if (f.left > 0) {
-                --f.left;
-                if (++f.i == f.t.n) {
-                    f.i = 0;
-                    if (f.left > 0) next_tile<kUnit>(a, work, f.t, f.left);
-                }
+            if (f.t.n > 0 && ++f.i == f.t.n) {
+                f.i = 0;
+                next_tile<kUnit, kCost>(a, work, f.t);
             }
             f_page = look_up();
         };
@@ -530,21 +521,12 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
                 __syncthreads();
             }
             // ---- out: finished rows, or a partial ------------------------------------
-            const bool begins = t.u0 == 0, ends = t.u0 + t.n >= t.units;
-            const int slot = slot0 + (begins ? 1 : 0);
-            const bool whole = begins && ends;
-            if (!whole) {
-                if (begins) wrote1 = true;
-                else wrote0 = true;
-                if (threadIdx.x == 0) {
-                    PartInfo pi;
-                    pi.q0 = t.q.q0;
-                    pi.packed0 = packed0;
-                    pi.packed_end = min(packed0 + kRows, packed);
-                    pi.head = t.head;
-                    pi.state = kPartUsed | (ends ? kPartLast : 0);
-                    a.parts.info[slot] = pi;
-                }
+            const PartPlace place = part_place(t);
+            const bool whole = place.whole;
+            const int slot = place.slot;
+            if (!whole && place.begins) {
+                open = true;
+                if (threadIdx.x == 0) note_open<kCost>(a, work, t);
             }
             for (int e = threadIdx.x; e < kRows * (HD / 8); e += kThreads) {
                 const int r = e / (HD / 8), c = e % (HD / 8);
@@ -579,14 +561,12 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
                 }
             }
             __syncthreads();
-            left -= t.n;
-            if (left <= 0) break;
-            next_tile<kUnit>(a, work, t, left);
+            next_tile<kUnit, kCost>(a, work, t);
+            if (t.n <= 0) break;
         }
         cp_wait<0>();
     }
-    if (!wrote0) store_part_none(a.parts, slot0);
-    if (!wrote1) store_part_none(a.parts, slot0 + 1);
+    if (!open && threadIdx.x == 0) a.parts.info[blockIdx.x].n = 0;
 }
 
 // What the join takes: the partials of the few-rows kernel's CTAs and of the
@@ -599,93 +579,107 @@ struct JoinArgs {
     int n_cta[2];
 };
 
-// Adds up the tile that begins in a CTA's slot 1 and goes on in the slots 0 of
-// the CTAs after it; blockIdx.x counts the CTAs of the first kernel, then those
-// of the second.  Few parts: a warp per row, gridDim.y blocks share the rows.
-// Many parts (a long sequence alone): the block's four warps take a row's
-// parts in turn.  The grid is small on purpose: most CTAs left no open tile,
-// and 7,296 blocks that only look cost 6 us, 912 cost less than 2.
+// Adds up the tile that a CTA left open: its slot 1 and the slots 0 of the
+// CTAs after it.  blockIdx.x counts the CTAs of the first kernel, then those
+// of the second.  HD / 4 threads take a row, four dims each; with many parts
+// (a long sequence alone) four such groups share a row's parts.  The kernel is
+// a chain of latencies (which tile, its maxima, its rows): every load of a
+// step is issued before the first is used, and the grid is small, since most
+// CTAs left nothing open (7,296 blocks that only look cost 6 us, 912 less
+// than 2).
 template <int HD, bool BF16>
-__global__ void __launch_bounds__(128) k_attn_join(const __grid_constant__ JoinArgs a) {
-    constexpr int kV = HD / 32;     // dims per lane
-    __shared__ float so[4][HD], sl[4];
+__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ JoinArgs a) {
+    constexpr int kT = HD / 4, kGroups = 256 / kT, kAhead = 8;
+    __shared__ float4 so[256];
+    __shared__ float sm_[kGroups], sl[kGroups];
     pdl_launch_dependents();
     pdl_wait();
     const int which = (int)blockIdx.x >= a.n_cta[0];
-    const int c0 = blockIdx.x - (which ? a.n_cta[0] : 0), n_cta = a.n_cta[which];
+    const int c0 = blockIdx.x - (which ? a.n_cta[0] : 0);
     const Parts& parts = a.parts[which];
-    const PartInfo first = parts.info[2 * c0 + 1];
-    if (first.state == kPartNone) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rows = parts.rows;
-    // Parts: slot 2 c0 + 1, then slots 2 c of the following CTAs up to the one
-    // that ends the tile; 32 CTAs are looked at at a time.
-    int n = 1;
-    for (int c = c0 + 1; c < n_cta; c += 32) {
-        const int st = c + lane < n_cta ? parts.info[2 * (c + lane)].state : kPartNone;
-        const unsigned stop = __ballot_sync(0xffffffffu, st == kPartNone || (st & kPartLast));
-        if (stop) {
-            const int k = __ffs(stop) - 1;
-            n += k + (__shfl_sync(0xffffffffu, st, k) != kPartNone);
-            break;
-        }
-        n += 32;
-    }
-    const bool together = n > 8;
-    const int step = together ? 1 : 4;
-    const auto slot = [&](int k) { return k == 0 ? 2 * c0 + 1 : 2 * (c0 + k); };
-    for (int r0 = blockIdx.y * step; first.packed0 + r0 < first.packed_end; r0 += gridDim.y * step) {
-        const int r = together ? r0 : r0 + warp;
-        const bool in = first.packed0 + r < first.packed_end;
-        float top = -INFINITY, sum = 0.f, acc[kV];
-#pragma unroll
-        for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+    const PartInfo info = parts.info[c0];
+    if (info.n == 0) return;
+    const int g = threadIdx.x / kT, d = threadIdx.x % kT;
+    const int rows = parts.rows, n = min(info.n, a.n_cta[which] - c0);
+    const int share = n > kAhead ? 4 : 1;                  // groups per row
+    const int sub = g % share;
+    const int at_once = kGroups / share;
+    // Every thread takes every turn (the barriers below).
+    for (int r0 = blockIdx.y * at_once; info.packed0 + r0 < info.packed_end; r0 += gridDim.y * at_once) {
+        const int r = r0 + g / share;
+        const bool in = info.packed0 + r < info.packed_end;
+        float top = -INFINITY, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (in) {
-            for (int k = lane; k < n; k += 32) top = fmaxf(top, parts.ml[(long long)slot(k) * 2 * rows + r]);
-            top = warp_max(top);
-            const float base = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-            for (int k = together ? warp : 0; k < n; k += step == 1 ? 4 : 1) {
-                const float* ml = parts.ml + (long long)slot(k) * 2 * rows + r;
-                const float w = ex2(ml[0] - base);
-                sum = fmaf(ml[rows], w, sum);
-                const float* o = parts.o + ((long long)slot(k) * rows + r) * HD + kV * lane;
-                if constexpr (kV == 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(o);
-                    acc[0] = fmaf(x.x, w, acc[0]);
-                    acc[1] = fmaf(x.y, w, acc[1]);
-                    acc[2] = fmaf(x.z, w, acc[2]);
-                    acc[3] = fmaf(x.w, w, acc[3]);
-                } else {
-                    const float2 x = *reinterpret_cast<const float2*>(o);
-                    acc[0] = fmaf(x.x, w, acc[0]);
-                    acc[1] = fmaf(x.y, w, acc[1]);
+            for (int k0 = sub; k0 < n; k0 += kAhead * share) {
+                float m[kAhead], l[kAhead];
+                float4 o[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int k = k0 + i * share;
+                    m[i] = -INFINITY;
+                    l[i] = 0.f;
+                    o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (k < n) {
+                        const long long slot = k == 0 ? 2 * c0 + 1 : 2 * (c0 + k);
+                        m[i] = parts.ml[slot * 2 * rows + r];
+                        l[i] = parts.ml[(slot * 2 + 1) * rows + r];
+                        o[i] = reinterpret_cast<const float4*>(parts.o + (slot * rows + r) * HD)[d];
+                    }
+                }
+                float t = top;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) t = fmaxf(t, m[i]);
+                const float base = t == -INFINITY ? 0.f : t, old = ex2(top - base);
+                top = t;
+                sum *= old;
+                acc.x *= old;
+                acc.y *= old;
+                acc.z *= old;
+                acc.w *= old;
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const float w = ex2(m[i] - base);
+                    sum = fmaf(l[i], w, sum);
+                    acc.x = fmaf(o[i].x, w, acc.x);
+                    acc.y = fmaf(o[i].y, w, acc.y);
+                    acc.z = fmaf(o[i].z, w, acc.z);
+                    acc.w = fmaf(o[i].w, w, acc.w);
                 }
             }
         }
-        if (together) {
-#pragma unroll
-            for (int e = 0; e < kV; ++e) so[warp][kV * lane + e] = acc[e];
-            if (lane == 0) sl[warp] = sum;
+        if (share > 1) {
+            so[threadIdx.x] = acc;
+            if (d == 0) {
+                sm_[g] = top;
+                sl[g] = sum;
+            }
             __syncthreads();
-            sum = (sl[0] + sl[1]) + (sl[2] + sl[3]);
-#pragma unroll
-            for (int e = 0; e < kV; ++e) {
-                const int d = kV * lane + e;
-                acc[e] = (so[0][d] + so[1][d]) + (so[2][d] + so[3][d]);
+            const int first = g - sub;
+            float t = -INFINITY;
+            for (int i = 0; i < share; ++i) t = fmaxf(t, sm_[first + i]);
+            const float base = t == -INFINITY ? 0.f : t;
+            top = t;
+            sum = 0.f;
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < share; ++i) {
+                const float w = ex2(sm_[first + i] - base);
+                const float4 o = so[(first + i) * kT + d];
+                sum = fmaf(sl[first + i], w, sum);
+                acc.x = fmaf(o.x, w, acc.x);
+                acc.y = fmaf(o.y, w, acc.y);
+                acc.z = fmaf(o.z, w, acc.z);
+                acc.w = fmaf(o.w, w, acc.w);
             }
             __syncthreads();
         }
-        if (!in || (together && warp)) continue;
-        const int i = first.packed0 + r;
-        const int row = first.q0 + i / a.group, qh = first.head * a.group + i % a.group;
+        if (!in || sub) continue;
+        const int i = info.packed0 + r;
+        const int row = info.q0 + i / a.group, qh = info.head * a.group + i % a.group;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        char* dst = a.out.data + (long long)row * a.out.row_bytes + (long long)qh * a.out.head_bytes + 2 * kV * lane;
-        if constexpr (kV == 4)
-            *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(acc[0] * inv, acc[1] * inv), pack2<BF16>(acc[2] * inv, acc[3] * inv));
-        else
-            *reinterpret_cast<uint32_t*>(dst) = pack2<BF16>(acc[0] * inv, acc[1] * inv);
-        if (a.lse && lane == 0)
+        *reinterpret_cast<uint2*>(a.out.data + (long long)row * a.out.row_bytes + (long long)qh * a.out.head_bytes + 8 * d) =
+            make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+        if (a.lse && d == 0)
             a.lse[(long long)row * a.n_head + qh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     }
 }
@@ -800,12 +794,12 @@ cudaError_t enqueue_attention(const Pool& kv, const Batch& b, const AttnCall& c,
         j.parts[1] = a.parts;
         j.n_cta[1] = n_sm;
     }
-    const dim3 grid(j.n_cta[0] + j.n_cta[1], plan.tc ? 8 : 2);
+    const dim3 grid(j.n_cta[0] + j.n_cta[1], plan.tc ? 8 : 2), block(256);
     if (c.head_dim == 64)
-        return bf16 ? launch_pdl(k_attn_join<64, true>, grid, dim3(128), 0, st, j)
-                    : launch_pdl(k_attn_join<64, false>, grid, dim3(128), 0, st, j);
-    return bf16 ? launch_pdl(k_attn_join<128, true>, grid, dim3(128), 0, st, j)
-                : launch_pdl(k_attn_join<128, false>, grid, dim3(128), 0, st, j);
+        return bf16 ? launch_pdl(k_attn_join<64, true>, grid, block, 0, st, j)
+                    : launch_pdl(k_attn_join<64, false>, grid, block, 0, st, j);
+    return bf16 ? launch_pdl(k_attn_join<128, true>, grid, block, 0, st, j)
+                : launch_pdl(k_attn_join<128, false>, grid, block, 0, st, j);
 }
 
 }  // namespace paged

@@ -20,11 +20,13 @@
 // and the tensor core takes P from there: O += P V.  While the warpgroup of
 // one half is at its softmax, the products of the other half run.
 //
-// Warps: 0-3 softmax of A, 4-7 of B, 8 issues the products, 9 feeds (10 and 11
-// fill the third warpgroup).  TMEM
-// (512 columns): S_A, S_B at 0 and 128; O_A, O_B from 256; P in columns of
-// its own for head_dim 64, over its own S for head_dim 128, where S of the
-// next unit is issued once P V has completed.
+// Warps: 0-3 softmax of A, 4-7 of B, 8 and 10 issue the products of A and B
+// (waits and commits cost an issuing thread some 150 cycles each, one thread
+// for both halves left the tensor pipe idle half the time), 9 feeds (11 fills
+// the third warpgroup).  TMEM (512 columns): S_A, S_B at 0 and 128; O_A, O_B
+// from 256.  head_dim 64 has columns of their own for P, so S of the next unit
+// is made while P of this one is; for head_dim 128 P lies over its own S and S
+// of the next unit follows P V.  P is handed over in two parts of 64 positions.
 //
 // 8-bit pages: four more warps (12-15) read the codes, widen them to exact
 // 16-bit values (of the queries' type) and store the swizzled tiles that TMA
@@ -51,6 +53,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kUnit = 128;                 // positions per unit
+constexpr int kCost = 2;                   // slots of a tile beside its units (paged.cuh)
 enum Kind { kSame16, kInt8, kE4m3 };
 // Registers per thread (setmaxnreg): a softmax thread holds a row of S.
 // 16-bit pages: 384 threads launched with 168 (64,512 in all),
@@ -63,6 +66,7 @@ struct Split {
     static constexpr int kOther = K == kSame16 ? 104 : 72;
 };
 constexpr int kFeeders = 4;                // warps that widen 8-bit codes
+constexpr int kStaging = 8 * 2048;         // output rows on their way, 2 KB per softmax warp
 constexpr int kScaleUnits = 4;             // units whose scales are kept (8-bit pages)
 constexpr int kMaxStages = 12, kMaxStages8 = 6;
 constexpr int kHalfBytes = 128 * 128;      // 128 rows of 64 16-bit elements
@@ -71,7 +75,7 @@ constexpr float kSlack = 8.f;              // log2 of the growth that is left in
 
 struct TcSmem {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], tail, drain;
+    uint64_t q_full, q_empty, s_full[2], s_read[2], p_lo[2], p_hi[2], o_full[2], turn[2], tail, drain[2];
     unsigned bad[8];                       // per unit (mod 8): its positions in bad pages, 16 per bit
     int g[kScaleUnits];                    // 8-bit pages, per unit (mod 4): log2 of G
     uint32_t tmem_slot;
@@ -86,21 +90,28 @@ struct TcArgs {
     int sub_rows;         // R
     int stages;           // ring stages of one K or V tile
     int kv_rank[3];       // tensor-map dims (1..3) of position, head, page
-    int min_units;
+    int min_slots;
 };
 
-__device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity, TcSmem& sm, int* guard) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
+// Waits for the phase of parity `parity`, at most about kWaitNs: the SM's own
+// clock is read (a read of the global timer costs a large part of a unit's
+// time).  False once this or another wait of the block has given up.
+constexpr long long kWaitClocks = (long long)kWaitNs * 2;      // 2 s or more at up to 2 GHz
+__device__ __forceinline__ bool wait_slow(uint64_t* bar, unsigned parity, TcSmem& sm, int* guard) {
+    const long long t0 = clock64();
     for (;;) {
-        if (mbar_try_wait(bar, parity)) return true;
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
         if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
-        if (global_ns() - t0 > kWaitNs) {
+        if (clock64() - t0 > kWaitClocks) {
             sm.abort = 1;
             raise_guard(guard, kGuardTimeout);
             return false;
         }
     }
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity, TcSmem& sm, int* guard) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, sm, guard);
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
@@ -184,6 +195,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// A place in the ring of K and V tiles: entries are stored and used in order.
+struct Cursor {
+    unsigned stage = 0, round = 0;
+    __device__ __forceinline__ void next(unsigned stages) {
+        if (++stage == stages) {
+            stage = 0;
+            ++round;
+        }
+    }
+};
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
@@ -219,16 +241,63 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// Writes one finished row's 32 dims, or a partial's.
-template <bool BF16>
-__device__ __forceinline__ void put_row32(char* dst, const uint32_t (&o)[32], float inv) {
+__device__ __forceinline__ float4 lds4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {
+    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
+        "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+
+// Scores of 32 positions times k's scales.
+__device__ __forceinline__ void scale_scores(uint32_t (&s)[32], uint32_t at) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t w[4];
+    for (int e = 0; e < 32; e += 4) {
+        const float4 ks = lds4(at + 4 * e);
+        float y[4] = {__uint_as_float(s[e]), __uint_as_float(s[e + 1]), __uint_as_float(s[e + 2]),
+                      __uint_as_float(s[e + 3])};
+        mul2(y[0], y[1], ks.x, ks.y);
+        mul2(y[2], y[3], ks.z, ks.w);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[e] = pack2<BF16>(__uint_as_float(o[8 * c + 2 * e]) * inv, __uint_as_float(o[8 * c + 2 * e + 1]) * inv);
-        reinterpret_cast<uint4*>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 4; ++i) s[e + i] = __float_as_uint(y[i]);
+    }
+}
+__device__ __forceinline__ void top2(float& v, uint32_t a, uint32_t b) {
+    v = max3(v, __uint_as_float(a), __uint_as_float(b));
+}
+// Two scores to weights, in place: 2^(score * scale + base).
+__device__ __forceinline__ void weigh2(uint32_t& a, uint32_t& b, float scale, float base) {
+    float y = __uint_as_float(a), z = __uint_as_float(b);
+    fma2(y, z, scale, base);
+    a = __float_as_uint(ex2(y));
+    b = __float_as_uint(ex2(z));
+}
+
+// 64 bytes of each of the warp's 32 rows (lane l holds row l's, dst its
+// address, null for a row that is not written) to offset `off` of the rows.
+__device__ __forceinline__ void put_rows64(uint32_t stage, const uint32_t (&w)[16], char* dst, int off, int lane) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4)),
+                     "r"(w[4 * j]), "r"(w[4 * j + 1]), "r"(w[4 * j + 2]), "r"(w[4 * j + 3])
+                     : "memory");
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2), j = lane & 3;
+        char* to = reinterpret_cast<char*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(stage + r * 64 + ((j ^ (r >> 1 & 3)) << 4))
+                     : "memory");
+        if (to) *reinterpret_cast<uint4*>(to + off + 16 * j) = v;
     }
 }
 
@@ -287,18 +356,6 @@ __device__ __forceinline__ bool feeders_agree(bool ok) {
     return all != 0;
 }
 
-__device__ __forceinline__ float4 lds4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {
-    asm("{\n\t.reg .b64 p, q;\n\tmov.b64 p, {%0, %1};\n\tmov.b64 q, {%2, %3};\n\t"
-        "mul.rn.f32x2 p, p, q;\n\tmov.b64 {%0, %1}, p;\n\t}"
-        : "+f"(x), "+f"(y)
-        : "f"(a), "f"(b));
-}
-
 template <int HD, bool BF16, Kind K>
 __global__ void __launch_bounds__(Split<K>::kThreads, 1)
     k_paged_attn_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -307,14 +364,16 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
     constexpr int kHalves = HD / 64;
     constexpr int kTileBytes = kHalves * kHalfBytes;
     constexpr bool k8 = K != kSame16;
+    constexpr bool kOverlay = HD == 128;        // P lies over S
     const AttnArgs& a = args.a;
     extern __shared__ unsigned char tc_smem_raw[];
     const uint32_t pad = (1024u - (smem_addr(tc_smem_raw) & 1023u)) & 1023u;
     TcSmem& sm = *reinterpret_cast<TcSmem*>(tc_smem_raw + pad);
     const uint32_t q_tiles = smem_addr(&sm) + kHead;                 // A, B
     const uint32_t ring = q_tiles + 2 * kTileBytes;
-    const uint32_t scales = ring + args.stages * kTileBytes;         // 8-bit: [kScaleUnits][k, v / G][kUnit] f32
-    long long* prefix = reinterpret_cast<long long*>(tc_smem_raw + pad + kHead + (2 + args.stages) * kTileBytes +
+    const uint32_t staging = ring + args.stages * kTileBytes;        // 2 KB per softmax warp
+    const uint32_t scales = staging + kStaging;                      // 8-bit: [kScaleUnits][k, v / G][kUnit] f32
+    long long* prefix = reinterpret_cast<long long*>(tc_smem_raw + pad + kHead + (2 + args.stages) * kTileBytes + kStaging +
                                                      (k8 ? kScaleUnits * 2 * kUnit * 4 : 0));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -322,17 +381,20 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < args.stages; ++i) {
             mbar_init(&sm.full[i], k8 ? kFeeders : 1);
-            mbar_init(&sm.empty[i], 1);
+            mbar_init(&sm.empty[i], 2);
         }
         mbar_init(&sm.q_full, 1);
-        mbar_init(&sm.q_empty, 1);
+        mbar_init(&sm.q_empty, 2);
         for (int x = 0; x < 2; ++x) {
             mbar_init(&sm.s_full[x], 1);
-            mbar_init(&sm.p_full[x], 128);
+            mbar_init(&sm.s_read[x], 128);
+            mbar_init(&sm.p_lo[x], 128);
+            mbar_init(&sm.p_hi[x], 128);
             mbar_init(&sm.o_full[x], 1);
+            mbar_init(&sm.turn[x], 1);
+            mbar_init(&sm.drain[x], 1);
         }
         mbar_init(&sm.tail, 1);
-        mbar_init(&sm.drain, 1);
         mbar_init_fence();
         sm.abort = 0;
     }
@@ -344,16 +406,14 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
             tma_prefetch_desc(&tm_v);
         }
     }
-    const WorkList work = build_work<kUnit>(a, prefix, args.min_units);
+    const WorkList work = build_work<kUnit, kCost>(a, prefix, args.min_slots);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_slot;
-    long long left = work.end - work.begin;
-    const int slot0 = 2 * blockIdx.x;
-    bool wrote0 = false, wrote1 = false;
-    if (left > 0) {
-        Tile t = find_tile<kUnit>(a, work, work.begin, left);
+    bool open = false;
+    if (work.begin < work.end) {
+        Tile t = find_tile<kUnit, kCost>(a, work);
         if (warp < 8) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Split<K>::kSoftmax));
             // ---- softmax of half x --------------------------------------------------
@@ -363,6 +423,8 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
             const float sc = a.scale_log2;
             unsigned n_s = 0;          // units of this half so far
             unsigned unit = 0;         // units of the CTA before this tile
+            Cursor cur;                // K of the current unit; V follows
+            unsigned v_stage = 0;      // V of the unit before
             bool ok = true;
             while (ok) {
                 const int packed0 = t.t * a.tile, packed = t.q.n * a.group;
@@ -382,58 +444,114 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) tmem_ld32_async(t_s + 32 * c, s[c]);
                         const unsigned bad = sm.bad[(unit + u) & 7];
+                        if (rl == 0) {
+                            // This half is done with the unit's K tile, with the queries after the
+                            // last one, and (S was issued after the last P V had completed) with
+                            // the V tile before.
+                            mbar_arrive(&sm.empty[cur.stage]);
+                            if (u + 1 == t.n) mbar_arrive(&sm.q_empty);
+                            if (kOverlay && u > 0) mbar_arrive(&sm.empty[v_stage]);
+                        }
+                        cur.next(args.stages);
                         tmem_ld_wait();
 #pragma unroll
                         for (int c = 0; c < 4; ++c) pin32(s[c]);
+                        if constexpr (!kOverlay) {
+                            tc_fence_before();
+                            mbar_arrive(&sm.s_read[x]);
+                        }
                         const uint32_t at = scales + ((unit + u) % kScaleUnits) * (2 * kUnit * 4);
                         if constexpr (k8) {
 #pragma unroll
-                            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                                for (int e = 0; e < 32; e += 4) {
-                                    const float4 ks = lds4(at + 4 * (32 * c + e));
-                                    float y[4] = {__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]),
-                                                  __uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3])};
-                                    mul2(y[0], y[1], ks.x, ks.y);
-                                    mul2(y[2], y[3], ks.z, ks.w);
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) s[c][e + i] = __float_as_uint(y[i]);
-                                }
+                            for (int c = 0; c < 4; ++c) scale_scores(s[c], at + 128 * c);
                         }
-                        if (key0 + kUnit - 1 > sure || bad) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (key0 + 32 * c + e > lim || (bad >> (2 * c + e / 16) & 1)) s[c][e] = 0xff800000u;
-                        }
+                        // With a reference already there, the weights of the first 64
+                        // positions are made against it while the maximum is still being
+                        // taken: it has to move only if some score has outgrown it.
+                        const bool cut = key0 + kUnit - 1 > sure || bad;
+                        const bool ahead = kOverlay && !k8 && u > 0 && !cut && !__any_sync(0xffffffffu, m == -INFINITY);
                         float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2)
-                                v[e / 2 & 3] = max3(v[e / 2 & 3], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
-                        const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * sc;
-                        // A new reference once the maximum has outgrown the old one.
-                        const bool move = top > m + kSlack;
                         float corr = 1.f;
-                        if (move) {
-                            corr = ex2(m - top);
-                            m = top;
-                            l0 *= corr;
-                            l1 *= corr;
+                        bool moved = false;
+                        const auto settle = [&]() {
+                            const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * sc;
+                            const bool move = top > m + kSlack;
+                            if (move) {
+                                corr = ex2(m - top);
+                                m = top;
+                                l0 *= corr;
+                                l1 *= corr;
+                            }
+                            moved = __any_sync(0xffffffffu, move);
+                        };
+                        if (!ahead) {
+                            if (cut) {
+                                const int last = lim - key0;      // last position of the unit the row sees
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    if (__any_sync(0xffffffffu, last < 32 * c + 31)) {
+#pragma unroll
+                                        for (int e = 0; e < 32; ++e)
+                                            if (32 * c + e > last) s[c][e] = 0xff800000u;
+                                    }
+                                if (bad) {
+#pragma unroll
+                                    for (int c = 0; c < 8; ++c)
+                                        if (bad >> c & 1)
+#pragma unroll
+                                            for (int e = 0; e < 16; ++e) s[c / 2][16 * (c % 2) + e] = 0xff800000u;
+                                }
+                            }
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) top2(v[e / 2 & 3], s[c][e], s[c][e + 1]);
+                            settle();
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) weigh2(s[c][e], s[c][e + 1], sc, m == -INFINITY ? 0.f : -m);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    top2(v[e / 2 & 1], s[c][e], s[c][e + 1]);
+                                    top2(v[2 + (e / 2 & 1)], s[2 + c][e], s[2 + c][e + 1]);
+                                    weigh2(s[c][e], s[c][e + 1], sc, -m);
+                                }
+                            settle();
+                            if (moved) {
+                                // The scores are still in TMEM: P has not been stored yet.
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) tmem_ld32_async(t_s + 32 * c, s[c]);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    pin32(s[c]);
+                                    if constexpr (k8) scale_scores(s[c], at + 128 * c);
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 2) weigh2(s[c][e], s[c][e + 1], sc, -m);
+                                }
+                            }
                         }
-                        bool scale_o = __any_sync(0xffffffffu, move);
+                        bool scale_o = moved;
                         if constexpr (k8) {
                             const int ng = sm.g[(unit + u) % kScaleUnits];
                             corr *= pow2i(max(g - ng, -126));
                             scale_o = scale_o || ng != g;
                             g = ng;
                         }
-                        if (u > 0 && scale_o) {
+                        if (u > 0 && (!kOverlay || scale_o)) {
+                            // P V of the unit before: P's columns and O are free after it.
                             ok = __all_sync(0xffffffffu, wait(&sm.o_full[x], (n_s - 1) & 1, sm, a.b.guard));
                             if (!ok) break;
                             tc_fence_after();
+                            if (!kOverlay && rl == 0) mbar_arrive(&sm.empty[v_stage]);
+                        }
+                        v_stage = cur.stage;
+                        cur.next(args.stages);
+                        if (u > 0 && scale_o) {
 #pragma unroll 1
                             for (int c = 0; c < HD / 32; ++c) {
                                 uint32_t o[32];
@@ -452,11 +570,10 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
                             [[maybe_unused]] float4 vs;
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
-                                float y = __uint_as_float(s[2 * c + e / 16][2 * e % 32]);
-                                float z = __uint_as_float(s[2 * c + e / 16][2 * e % 32 + 1]);
-                                fma2(y, z, sc, base);
-                                y = ex2(y);
-                                z = ex2(z);
+                                uint32_t& sy = s[2 * c + e / 16][2 * e % 32];
+                                uint32_t& sz = s[2 * c + e / 16][2 * e % 32 + 1];
+                                if (c) weigh2(sy, sz, sc, base);
+                                float y = __uint_as_float(sy), z = __uint_as_float(sz);
                                 add2(l0, l1, y, z);
                                 if constexpr (k8) {
                                     if (e % 2 == 0) vs = lds4(at + 4 * kUnit + 4 * (64 * c + 2 * e));
@@ -465,143 +582,174 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
                                 p[e] = pack2<BF16>(y, z);
                             }
                             tmem_st32(t_p + 32 * c, p);
+                            tmem_st_wait();
+                            tc_fence_before();
+                            mbar_arrive(c ? &sm.p_hi[x] : &sm.p_lo[x]);
                         }
-                        tmem_st_wait();
-                        tc_fence_before();
-                        mbar_arrive(&sm.p_full[x]);
                     }
                     if (!ok) break;
                     // ---- the half's rows ------------------------------------------------
                     ok = __all_sync(0xffffffffu, wait(&sm.o_full[x], (n_s - 1) & 1, sm, a.b.guard));
                     if (!ok) break;
                     tc_fence_after();
+                    if (rl == 0) mbar_arrive(&sm.empty[v_stage]);
                     const float l = l0 + l1, unit_g = k8 ? pow2i(g) : 1.f;
-                    const bool begins = t.u0 == 0, ends = t.u0 + t.n >= t.units;
-                    const int slot = slot0 + (begins ? 1 : 0), r = x * args.sub + rl;
-                    if (begins && ends) {
-                        const float inv = l == 0.f ? 0.f : unit_g / l;
+                    const PartPlace place = part_place(t);
+                    const int slot = place.slot, r = x * args.sub + rl;
+                    // Rows go out through the warp's staging buffer: 64 bytes of each of its 32 rows
+                    // at a time, written a row per lane and stored four lanes a row (a row per lane
+                    // straight to memory touches 32 lines a store and holds the load / store unit
+                    // for 5,000 cycles a tile).
+                    const bool whole = place.whole;
+                    const float f = !whole ? unit_g : l == 0.f ? 0.f : unit_g / l;
+                    char* dst;
+                    if (whole) {
                         const int row = t.q.q0 + i / a.group, qh = t.head * a.group + i % a.group;
-                        char* dst = a.out.data + (long long)row * a.out.row_bytes + (long long)qh * a.out.head_bytes;
-#pragma unroll
-                        for (int c = 0; c < HD / 32; ++c) {
-                            uint32_t o[32];
-                            tmem_ld32_async(t_o + 32 * c, o);
-                            tmem_ld_wait();
-                            pin32(o);
-                            if (live) put_row32<BF16>(dst + 64 * c, o, inv);
-                        }
+                        dst = a.out.data + (long long)row * a.out.row_bytes + (long long)qh * a.out.head_bytes;
                         if (live && a.lse)
                             a.lse[(long long)row * a.n_head + qh] =
                                 l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                     } else {
-                        float* po = a.parts.o + ((long long)slot * a.parts.rows + r) * HD;
-#pragma unroll
-                        for (int c = 0; c < HD / 32; ++c) {
-                            uint32_t o[32];
-                            tmem_ld32_async(t_o + 32 * c, o);
-                            tmem_ld_wait();
-                            pin32(o);
-                            if (live)
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    reinterpret_cast<float4*>(po + 32 * c)[e] = make_float4(
-                                        __uint_as_float(o[4 * e]) * unit_g, __uint_as_float(o[4 * e + 1]) * unit_g,
-                                        __uint_as_float(o[4 * e + 2]) * unit_g, __uint_as_float(o[4 * e + 3]) * unit_g);
-                        }
+                        dst = reinterpret_cast<char*>(a.parts.o + ((long long)slot * a.parts.rows + r) * HD);
                         if (live) {
                             a.parts.ml[(long long)slot * 2 * a.parts.rows + r] = m;
                             a.parts.ml[((long long)slot * 2 + 1) * a.parts.rows + r] = l;
                         }
-                        if (begins) wrote1 = true;
-                        else wrote0 = true;
-                        if (tid == 0) {
-                            PartInfo pi;
-                            pi.q0 = t.q.q0;
-                            pi.packed0 = packed0;
-                            pi.packed_end = min(packed0 + a.tile, packed);
-                            pi.head = t.head;
-                            pi.state = kPartUsed | (ends ? kPartLast : 0);
-                            a.parts.info[slot] = pi;
+                    }
+                    if (!live) dst = nullptr;
+                    const uint32_t stage = staging + 2048 * warp;
+#pragma unroll 1
+                    for (int c = 0; c < HD / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32_async(t_o + 32 * c, o);
+                        tmem_ld_wait();
+                        pin32(o);
+                        if (whole) {
+                            uint32_t w[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                w[e] = pack2<BF16>(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+                            put_rows64(stage, w, dst, 64 * c, lane);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            put_rows64(stage, reinterpret_cast<const uint32_t(&)[16]>(o[0]), dst, 128 * c, lane);
+                            put_rows64(stage, reinterpret_cast<const uint32_t(&)[16]>(o[16]), dst, 128 * c + 64, lane);
                         }
                     }
+                    if (!whole && place.begins) {
+                        open = true;
+                        if (tid == 0) note_open<kCost>(a, work, t);
+                    }
                     tc_fence_before();
+                } else {
+                    for (int u = 0; u < 2 * t.n; ++u) cur.next(args.stages);
                 }
                 unit += t.n;
-                left -= t.n;
-                if (left <= 0) break;
-                next_tile<kUnit>(a, work, t, left);
+                next_tile<kUnit, kCost>(a, work, t);
+                if (t.n <= 0) break;
             }
         } else {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<K>::kOther));
         }
-        if (warp == 8) {
-            // ---- products -------------------------------------------------------------
+        if (warp == 8 || warp == 10) {
+            // ---- products of half x ---------------------------------------------------
             if (lane == 0) {
                 constexpr uint32_t id_s = idesc16(128, kUnit, BF16, false), id_o = idesc16(128, HD, BF16, true);
-                unsigned n_u[2] = {0, 0}, seg = 0, ent = 0;
+                const int x = warp == 8 ? 0 : 1;
+                const uint64_t qd = desc_sw128(q_tiles + x * kTileBytes);
+                const uint32_t t_s = tmem + T::s(x), t_o = tmem + T::o(x), t_p = tmem + T::p(x);
+                unsigned n_u = 0, seg = 0;       // P V products so far; tiles
+                unsigned turns = 0;              // units of tiles with both halves so far
+                Cursor cur;
                 bool ok = true;
-                const auto stage_of = [&](unsigned e) { return e % (unsigned)args.stages; };
-                const auto landed = [&](unsigned e) {
-                    ok = ok && wait(&sm.full[stage_of(e)], (e / (unsigned)args.stages) & 1, sm, a.b.guard);
+                const auto landed = [&](const Cursor& c) {
+                    ok = ok && wait(&sm.full[c.stage], c.round & 1, sm, a.b.guard);
                 };
-                // S of half x against the K tile of ring entry e.
-                const auto issue_s = [&](int x, unsigned e) {
-                    if (n_u[x])
-                        ok = ok && wait(&sm.o_full[x], (n_u[x] - 1) & 1, sm, a.b.guard);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint64_t qd = desc_sw128(q_tiles + x * kTileBytes);
-                    const uint64_t kd = desc_sw128(ring + stage_of(e) * kTileBytes);
+                // S against the K tile at `cur`.
+                const auto issue_s = [&](bool hand_over) {
+                    const uint64_t kd = desc_sw128(ring + cur.stage * kTileBytes);
 #pragma unroll
                     for (int k = 0; k < HD / 16; ++k) {
+                        if (k == HD / 32 && hand_over) mbar_arrive(&sm.turn[x ^ 1]);
                         const uint32_t off = (uint32_t)((k / 4) * kHalfBytes + (k % 4) * 32) >> 4;
-                        mma_f16(tmem + T::s(x), qd + off, kd + off, id_s, k != 0 ? 1u : 0u);
+                        mma_f16(t_s, qd + off, kd + off, id_s, k != 0 ? 1u : 0u);
                     }
                     mma_commit(&sm.s_full[x]);
                 };
-                while (ok) {
-                    const int halves = t.t * a.tile + args.sub < t.q.n * a.group ? 2 : 1;
-                    ok = wait(&sm.q_full, seg & 1, sm, a.b.guard);
-                    ++seg;
-                    landed(ent);
-                    for (int x = 0; x < halves && ok; ++x) issue_s(x, ent);
-                    if (!ok) break;
-                    mma_commit(&sm.empty[stage_of(ent)]);
-                    if (t.n == 1) mma_commit(&sm.q_empty);
-                    ++ent;
-                    for (int u = 0; u < t.n; ++u) {
-                        const unsigned ev = ent;           // V of this unit; K of the next one follows
-                        landed(ev);
-                        if (u + 1 < t.n) landed(ev + 1);
-                        for (int x = 0; x < halves; ++x) {
-                            ok = ok && wait(&sm.p_full[x], n_u[x] & 1, sm, a.b.guard);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint64_t vd = desc_mn128(ring + stage_of(ev) * kTileBytes);
-#pragma unroll
-                            for (int k = 0; k < kUnit / 16; ++k)
-                                mma_ts(tmem + T::o(x), tmem + T::p(x) + 8 * k, vd + (2048 * k >> 4), id_o,
-                                       u > 0 || k > 0 ? 1u : 0u);
-                            mma_commit(&sm.o_full[x]);
-                            ++n_u[x];
-                            if (u + 1 < t.n) issue_s(x, ev + 1);
+                for (;; ++seg) {
+                    const bool both = t.t * a.tile + args.sub < t.q.n * a.group;
+                    ok = ok && wait(&sm.q_full, seg & 1, sm, a.b.guard);
+                    if (x == 1 && !both) {
+                        // No rows in this half: its share of releasing the ring all the same.
+                        for (int e = 0; e < 2 * t.n && ok; ++e) {
+                            landed(cur);
+                            if (ok) mbar_arrive(&sm.empty[cur.stage]);
+                            cur.next(args.stages);
                         }
+                        if (ok) mbar_arrive(&sm.q_empty);
+                    } else {
+                        landed(cur);
+                        if (kOverlay && n_u) ok = ok && wait(&sm.o_full[x], (n_u - 1) & 1, sm, a.b.guard);
                         if (!ok) break;
-                        mma_commit(&sm.empty[stage_of(ev)]);
-                        ++ent;
-                        if (u + 1 < t.n) {
-                            mma_commit(&sm.empty[stage_of(ev + 1)]);
-                            if (u + 2 == t.n) mma_commit(&sm.q_empty);
-                            ++ent;
+                        tc_fence_after();
+                        issue_s(false);
+                        cur.next(args.stages);
+                        for (int u = 0; u < t.n; ++u) {
+                            const Cursor v = cur;              // V of this unit; K of the next one follows
+                            const bool more = u + 1 < t.n;
+                            cur.next(args.stages);
+                            if (!kOverlay) {
+                                // S of the next unit once this one's is in registers.
+                                ok = ok && wait(&sm.s_read[x], n_u & 1, sm, a.b.guard);
+                                if (more) {
+                                    landed(cur);
+                                    if (!ok) break;
+                                    tc_fence_after();
+                                    issue_s(false);
+                                    cur.next(args.stages);
+                                }
+                            }
+                            landed(v);
+                            const uint64_t vd = desc_mn128(ring + v.stage * kTileBytes);
+                            // The first 64 positions' P V while the others' P is made.
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                ok = ok && wait(c ? &sm.p_hi[x] : &sm.p_lo[x], n_u & 1, sm, a.b.guard);
+                                if (kOverlay && c == 0 && both && (x == 1 || turns))
+                                    ok = ok && wait(&sm.turn[x], (x == 1 ? turns : turns - 1) & 1, sm, a.b.guard);
+                                if (!ok) break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int k = 4 * c; k < 4 * c + 4; ++k)
+                                    mma_ts(t_o, t_p + 8 * k, vd + (2048 * k >> 4), id_o, u > 0 || k > 0 ? 1u : 0u);
+                            }
+                            if (!ok) break;
+                            mma_commit(&sm.o_full[x]);
+                            ++n_u;
+                            if (kOverlay && more) {
+                                landed(cur);
+                                ok = ok && wait(&sm.o_full[x], (n_u - 1) & 1, sm, a.b.guard);
+                                if (!ok) break;
+                                tc_fence_after();
+                                // The other half's turn comes with the second part of S: P V and the
+                                // next S of one half run together, so that the halves' softmaxes fall
+                                // into each other's products.
+                                issue_s(both);
+                                cur.next(args.stages);
+                            }
+                            if (kOverlay && both) {
+                                if (!more) mbar_arrive(&sm.turn[x ^ 1]);
+                                ++turns;
+                            }
                         }
                     }
-                    left -= t.n;
-                    if (left <= 0 || !ok) break;
-                    next_tile<kUnit>(a, work, t, left);
+                    next_tile<kUnit, kCost>(a, work, t);
+                    if (t.n <= 0 || !ok) break;
                 }
                 if (!ok) {   // products in flight end before the tensor memory is given back
-                    mma_commit(&sm.drain);
-                    mbar_wait(&sm.drain, 0, kWaitNs);
+                    mma_commit(&sm.drain[x]);
+                    mbar_wait(&sm.drain[x], 0, kWaitNs);
                 }
             }
             __syncwarp();
@@ -609,7 +757,8 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
             // ---- feed: queries, and 16-bit pages ------------------------------------------
             const int page_rows = 1 << a.kv.page_shift, box = min(page_rows, kUnit), boxes = kUnit / box;
             const int p = lane / kHalves, h = lane % kHalves;
-            unsigned ent = 0, seg = 0, unit = 0, n_tail = 0;
+            unsigned seg = 0, unit = 0, n_tail = 0;
+            Cursor cur;
             bool ok = true;
             while (ok) {
                 const int halves = t.t * a.tile + args.sub < t.q.n * a.group ? 2 : 1;
@@ -644,8 +793,8 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
                     at[args.kv_rank[0]] = key & (page_rows - 1);
                     at[args.kv_rank[1]] = t.head;
                     at[args.kv_rank[2]] = page;
-                    for (int kv = 0; kv < 2 && ok; ++kv, ++ent) {
-                        const unsigned st = ent % (unsigned)args.stages, round = ent / (unsigned)args.stages;
+                    for (int kv = 0; kv < 2 && ok; ++kv, cur.next(args.stages)) {
+                        const unsigned st = cur.stage, round = cur.round;
                         if (round) ok = __all_sync(0xffffffffu, wait(&sm.empty[st], (round - 1) & 1, sm, a.b.guard));
                         if (!ok) break;
                         const uint32_t tile = ring + st * kTileBytes;
@@ -666,11 +815,13 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
                                 mbar_wait(&sm.tail, (n_tail - 1) & 1, kWaitNs);
                                 break;
                             }
-                            for (int r = lane; r < kUnit; r += 32)
+                            // Eight lanes a 128-byte row, four rows a store.
+                            for (int r = (bad ? 0 : max(0, t.keys - key0) & ~3) + (lane >> 3); r < kUnit; r += 4)
                                 if (key0 + r >= t.keys || (bad >> (r / 16) & 1))
-                                    for (int c = 0; c < 8 * kHalves; ++c)
+#pragma unroll
+                                    for (int c = 0; c < kHalves; ++c)
                                         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                                         tile + (c / 8) * kHalfBytes + r * 128 + (c % 8) * 16),
+                                                         tile + c * kHalfBytes + r * 128 + (lane & 7) * 16),
                                                      "r"(0)
                                                      : "memory");
                             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -679,13 +830,15 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
                         }
                     }
                 }
-                left -= t.n;
-                if (left <= 0 || !ok) break;
-                next_tile<kUnit>(a, work, t, left);
+                next_tile<kUnit, kCost>(a, work, t);
+                if (t.n <= 0 || !ok) break;
             }
-            if (!ok) {   // copies in flight land before the shared memory is given back
-                for (unsigned e = ent > (unsigned)args.stages ? ent - args.stages : 0; e < ent; ++e)
-                    mbar_wait(&sm.full[e % (unsigned)args.stages], (e / (unsigned)args.stages) & 1, kWaitNs);
+            if (!ok && !k8) {   // copies in flight land before the shared memory is given back
+                for (unsigned st = 0; st < (unsigned)args.stages; ++st)   // each stage's last entry
+                    if (st < cur.stage || cur.round)
+                        mbar_wait(&sm.full[st], (st < cur.stage ? cur.round : cur.round - 1) & 1, kWaitNs);
+            }
+            if (!ok) {
                 if (seg) mbar_wait(&sm.q_full, (seg - 1) & 1, kWaitNs);
             }
             __syncwarp();
@@ -695,7 +848,8 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
             // each 64-dim half: two adjacent rows' pieces fill all banks.
             const int e0 = tid - 384, piece = e0 & 3, row0 = e0 >> 2;
             constexpr int kPieces = 4 * kHalves;        // per thread and tile
-            unsigned ent = 0, unit = 0;
+            unsigned unit = 0;
+            Cursor cur;
             bool ok = true, stop = false;
             while (!stop) {
                 int g = -100;
@@ -741,9 +895,9 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
                         uint4 raw[kPieces];
 #pragma unroll
                         for (int i = 0; i < kPieces; ++i)
-                            raw[i] = in[i & 3] ? __ldg(reinterpret_cast<const uint4*>(base + src[i & 3] + 64 * (i >> 2)))
+                            raw[i] = in[i & 3] ? ld_stream_v4(base + src[i & 3] + 64 * (i >> 2))
                                                : make_uint4(0, 0, 0, 0);
-                        const unsigned st = ent % (unsigned)args.stages, round = ent / (unsigned)args.stages;
+                        const unsigned st = cur.stage, round = cur.round;
                         if (round && ok) ok = __all_sync(0xffffffffu, wait(&sm.empty[st], (round - 1) & 1, sm, a.b.guard));
                         if (kv == 0) {
                             // The slot of this unit's scales is free: with at most 6 stages the V tile stored last took
@@ -783,20 +937,16 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sm.full[st]);
-                        ++ent;
+                        cur.next(args.stages);
                     }
                     if (stop) break;
                 }
-                left -= t.n;
-                if (left <= 0) break;
-                next_tile<kUnit>(a, work, t, left);
+                next_tile<kUnit, kCost>(a, work, t);
+                if (t.n <= 0) break;
             }
         }
     }
-    if (tid == 0) {
-        if (!wrote0) a.parts.info[slot0].state = kPartNone;
-        if (!wrote1) a.parts.info[slot0 + 1].state = kPartNone;
-    }
+    if (tid == 0 && !open) a.parts.info[blockIdx.x].n = 0;
     tc_fence_before();
     __syncthreads();
     if (warp == 8) tmem_dealloc(tmem, kTmemCols);
@@ -862,7 +1012,7 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
     auto kern = k_paged_attn_tc<HD, BF16, K>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
-    const int rest = 8 * (args.a.b.n_seq + 1) + (K == kSame16 ? 0 : kScaleUnits * 2 * kUnit * 4);
+    const int rest = kStaging + 8 * (args.a.b.n_seq + 1) + (K == kSame16 ? 0 : kScaleUnits * 2 * kUnit * 4);
     const int room = 227 * 1024 - 1024 - kHead - rest - 2 * kTileBytes;
     args.stages = min(K == kSame16 ? kMaxStages : kMaxStages8, room / kTileBytes);
     const size_t smem = 1024 + kHead + (size_t)(2 + args.stages) * kTileBytes + rest;
@@ -904,7 +1054,7 @@ cudaError_t enqueue_attention_tc(const TcMaps& m, const AttnArgs& a, int format,
     args.sub = a.tile / 2;
     args.sub_rows = args.sub / a.group;
     for (int i = 0; i < 3; ++i) args.kv_rank[i] = m.kv_rank[i];
-    args.min_units = 2;
+    args.min_slots = kCost + 2;
     if (format == QWEN2_KV_INT8) return launch_hd<kInt8>(m, args, head_dim, bf16, n_sm, chained, st);
     if (format == QWEN2_KV_E4M3) return launch_hd<kE4m3>(m, args, head_dim, bf16, n_sm, chained, st);
     return launch_hd<kSame16>(m, args, head_dim, bf16, n_sm, chained, st);
