@@ -14,21 +14,26 @@
 // each half is R = 128 / group rows of the sequence with the group's heads
 // packed (a TMA box [R][group][64] lands as consecutive 128-byte rows), so a
 // K / V tile is read once for 2 R rows of all the group's heads.  Per unit of
-// 128 positions and half:  S = Q K^T into 128 columns of TMEM;
-// thread i of the half's warpgroup owns row i,
-// takes S into registers, writes P = 2^(s - m) as 16-bit pairs back to TMEM,
-// and the tensor core takes P from there: O += P V.  While the warpgroup of
-// one half is at its softmax, the products of the other half run.
+// 64 positions and half:  S = Q K^T into 64 columns of TMEM; thread i of the
+// half's warpgroup owns row i, takes S into registers, writes P = 2^(s - m)
+// as 16-bit pairs back over S, and the tensor core takes P from there:
+// O += P V.
 //
-// Warps: 0-3 softmax of A, 4-7 of B, 8 and 10 issue the products of A and B
-// (waits and commits cost an issuing thread some 150 cycles each, one thread
-// for both halves left the tensor pipe idle half the time), 9 feeds (11 fills
-// the third warpgroup).  TMEM (512 columns): S_A, S_B at 0 and 128; O_A, O_B
-// from 256.  head_dim 64 has columns of their own for P, so S of the next unit
-// is made while P of this one is; for head_dim 128 P lies over its own S and S
-// of the next unit follows P V.  P is handed over in two parts of 64 positions.
+// Each half has two S buffers: S of the next unit is there when a softmax
+// ends, and the softmaxes run back to back while the products of the unit
+// before and of the unit after next are made; S of a unit is issued once P V
+// of the unit two before, which used its buffer, has completed.  (One buffer
+// of 128 positions, with S behind P V, left the tensor pipe idle half the
+// time: softmax, P V, S and three hand-overs of 200 to 300 cycles in a row.)
 //
-// 8-bit pages: four more warps (12-15) read the codes, widen them to exact
+// Warps: 0-3 softmax of A, 4-7 of B; 8 and 9 issue S of A and B (8 also asks
+// for the queries), 10 and 11 P V (each wait or commit costs an issuing thread
+// 100 to 150 cycles and S of a unit waits for P V of an earlier one: one thread
+// for both products of a half took 2,160 cycles a unit, half of them waits).
+// Warp 12 feeds K and V.  TMEM (512 columns): S at 128 x + 64 b for buffer b of
+// half x, O from 256.
+//
+// 8-bit pages: four warps (12-15) read the codes, widen them to exact
 // 16-bit values (of the queries' type) and store the swizzled tiles that TMA
 // would have written.  The scales stay out of the products: k's multiplies the
 // scores, v's the probabilities, relative to G, the largest v scale so far
@@ -52,43 +57,41 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kUnit = 128;                 // positions per unit
-constexpr int kCost = 2;                   // slots of a tile beside its units (paged.cuh)
+constexpr int kUnit = 64;                  // positions per unit
+constexpr int kCost = 4;                   // slots of a tile beside its units (paged.cuh)
 enum Kind { kSame16, kInt8, kE4m3 };
-// Registers per thread (setmaxnreg): a softmax thread holds a row of S.
-// 16-bit pages: 384 threads launched with 168 (64,512 in all),
-// 2 * 128 * 200 + 128 * 104 = 64,512.  8-bit pages: 512 threads launched with
-// 128 (65,536), 2 * 128 * 184 + 2 * 128 * 72 = 65,536.
-template <Kind K>
-struct Split {
-    static constexpr int kThreads = K == kSame16 ? 384 : 512;
-    static constexpr int kSoftmax = K == kSame16 ? 200 : 184;
-    static constexpr int kOther = K == kSame16 ? 104 : 72;
-};
 constexpr int kFeeders = 4;                // warps that widen 8-bit codes
+template <Kind K>
+constexpr int kThreadsOf = K == kSame16 ? 416 : 512;
 constexpr int kStaging = 8 * 2048;         // output rows on their way, 2 KB per softmax warp
-constexpr int kScaleUnits = 4;             // units whose scales are kept (8-bit pages)
-constexpr int kMaxStages = 12, kMaxStages8 = 6;
-constexpr int kHalfBytes = 128 * 128;      // 128 rows of 64 16-bit elements
+constexpr int kLag = 8;                    // units whose scales and bad pages are kept
+constexpr int kMaxStages = 6;              // K tiles, and V tiles, in the ring: at most kLag - 2, so that a unit's
+                                           // slot is free when its K is stored: the V stored just before, of the
+                                           // unit two back, took the place of one whose P V had completed
+constexpr int kQBytes = 128 * 128;         // 128 rows of 64 16-bit elements
+constexpr int kHalfBytes = kUnit * 128;    // 64 positions of 64 16-bit elements
 constexpr uint32_t kTmemCols = 512;
 constexpr float kSlack = 8.f;              // log2 of the growth that is left in the weights
 
+// s_full, p_full and o_full have a barrier per buffer: unit n of a half is
+// phase n / 2 of barrier n % 2.  Up to two units are under way at once, and a
+// parity wait can tell only the current phase from the one before it.
 struct TcSmem {
-    uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t q_full, q_empty, s_full[2], s_read[2], p_lo[2], p_hi[2], o_full[2], turn[2], tail, drain[2];
-    unsigned bad[8];                       // per unit (mod 8): its positions in bad pages, 16 per bit
-    int g[kScaleUnits];                    // 8-bit pages, per unit (mod 4): log2 of G
+    uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
+    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_full[2][2], tail, drain[4];
+    unsigned bad[kLag];                    // per unit (mod kLag): its positions in bad pages, 16 per bit
+    int g[kLag];                           // 8-bit pages, per unit: log2 of G
     uint32_t tmem_slot;
     int abort;
 };
 constexpr int kHead = 1024;                // TcSmem, in front of the 1024-byte aligned tiles
-static_assert(sizeof(TcSmem) <= kHead - 64, "");      // the last 64 bytes: the feeders' reduction
+static_assert(sizeof(TcSmem) <= kHead, "");
 
 struct TcArgs {
     AttnArgs a;
     int sub;              // packed rows of a half: R * group
     int sub_rows;         // R
-    int stages;           // ring stages of one K or V tile
+    int k_stages, v_stages;
     int kv_rank[3];       // tensor-map dims (1..3) of position, head, page
     int min_slots;
 };
@@ -195,10 +198,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// A place in the ring of K and V tiles: entries are stored and used in order.
+// A place in the ring of K tiles or of V tiles: stored and used in order.
 struct Cursor {
-    unsigned stage = 0, round = 0;
-    __device__ __forceinline__ void next(unsigned stages) {
+    int stage = 0;
+    unsigned round = 0;
+    __device__ __forceinline__ void next(int stages) {
         if (++stage == stages) {
             stage = 0;
             ++round;
@@ -216,9 +220,8 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 template <int HD>
 struct Tmem {
-    static constexpr uint32_t s(int x) { return 128u * x; }
+    static constexpr uint32_t s(int x, int b) { return 128u * x + 64u * b; }
     static constexpr uint32_t o(int x) { return 256u + (uint32_t)HD * x; }
-    static constexpr uint32_t p(int x) { return HD == 64 ? 384u + 64u * x : s(x); }
 };
 
 // a * b + c on two floats at once.
@@ -266,17 +269,6 @@ __device__ __forceinline__ void scale_scores(uint32_t (&s)[32], uint32_t at) {
         for (int i = 0; i < 4; ++i) s[e + i] = __float_as_uint(y[i]);
     }
 }
-__device__ __forceinline__ void top2(float& v, uint32_t a, uint32_t b) {
-    v = max3(v, __uint_as_float(a), __uint_as_float(b));
-}
-// Two scores to weights, in place: 2^(score * scale + base).
-__device__ __forceinline__ void weigh2(uint32_t& a, uint32_t& b, float scale, float base) {
-    float y = __uint_as_float(a), z = __uint_as_float(b);
-    fma2(y, z, scale, base);
-    a = __float_as_uint(ex2(y));
-    b = __float_as_uint(ex2(z));
-}
-
 // 64 bytes of each of the warp's 32 rows (lane l holds row l's, dst its
 // address, null for a row that is not written) to offset `off` of the rows.
 __device__ __forceinline__ void put_rows64(uint32_t stage, const uint32_t (&w)[16], char* dst, int off, int lane) {
@@ -341,65 +333,52 @@ __device__ __forceinline__ int ceil_log2(float v) {
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
-// Barrier of the four feeding warps that tells all of them whether every one
-// got through its wait: they go on, or stop, together.
-__device__ __forceinline__ bool feeders_agree(bool ok) {
-    uint32_t all;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(all)
-        : "r"((uint32_t)ok)
-        : "memory");
-    return all != 0;
-}
-
 template <int HD, bool BF16, Kind K>
-__global__ void __launch_bounds__(Split<K>::kThreads, 1)
+__global__ void __launch_bounds__(kThreadsOf<K>, 1)
     k_paged_attn_tc(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TcArgs args) {
     using T = Tmem<HD>;
     constexpr int kHalves = HD / 64;
-    constexpr int kTileBytes = kHalves * kHalfBytes;
+    constexpr int kQTile = kHalves * kQBytes, kTile = kHalves * kHalfBytes;
     constexpr bool k8 = K != kSame16;
-    constexpr bool kOverlay = HD == 128;        // P lies over S
     const AttnArgs& a = args.a;
     extern __shared__ unsigned char tc_smem_raw[];
     const uint32_t pad = (1024u - (smem_addr(tc_smem_raw) & 1023u)) & 1023u;
     TcSmem& sm = *reinterpret_cast<TcSmem*>(tc_smem_raw + pad);
     const uint32_t q_tiles = smem_addr(&sm) + kHead;                 // A, B
-    const uint32_t ring = q_tiles + 2 * kTileBytes;
-    const uint32_t staging = ring + args.stages * kTileBytes;        // 2 KB per softmax warp
-    const uint32_t scales = staging + kStaging;                      // 8-bit: [kScaleUnits][k, v / G][kUnit] f32
-    long long* prefix = reinterpret_cast<long long*>(tc_smem_raw + pad + kHead + (2 + args.stages) * kTileBytes + kStaging +
-                                                     (k8 ? kScaleUnits * 2 * kUnit * 4 : 0));
+    const uint32_t k_ring = q_tiles + 2 * kQTile, v_ring = k_ring + args.k_stages * kTile;
+    const uint32_t staging = v_ring + args.v_stages * kTile;
+    const uint32_t scales = staging + kStaging;                      // 8-bit: [kLag][k, v / G][kUnit] f32
+    long long* prefix = reinterpret_cast<long long*>(tc_smem_raw + pad + kHead + 2 * kQTile +
+                                                     (args.k_stages + args.v_stages) * kTile + kStaging +
+                                                     (k8 ? kLag * 2 * kUnit * 4 : 0));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_launch_dependents();
     if (tid == 0) {
-        for (int i = 0; i < args.stages; ++i) {
-            mbar_init(&sm.full[i], k8 ? kFeeders : 1);
-            mbar_init(&sm.empty[i], 2);
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(&sm.k_full[i], k8 ? kFeeders : 1);
+            mbar_init(&sm.v_full[i], k8 ? kFeeders : 1);
+            mbar_init(&sm.k_empty[i], 2);
+            mbar_init(&sm.v_empty[i], 2);
         }
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_empty, 2);
         for (int x = 0; x < 2; ++x) {
-            mbar_init(&sm.s_full[x], 1);
-            mbar_init(&sm.s_read[x], 128);
-            mbar_init(&sm.p_lo[x], 128);
-            mbar_init(&sm.p_hi[x], 128);
-            mbar_init(&sm.o_full[x], 1);
-            mbar_init(&sm.turn[x], 1);
-            mbar_init(&sm.drain[x], 1);
+            mbar_init(&sm.s_full[x][0], 1);
+            mbar_init(&sm.s_full[x][1], 1);
+            mbar_init(&sm.p_full[x][0], 128);
+            mbar_init(&sm.p_full[x][1], 128);
+            mbar_init(&sm.o_full[x][0], 1);
+            mbar_init(&sm.o_full[x][1], 1);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&sm.drain[i], 1);
         mbar_init(&sm.tail, 1);
         mbar_init_fence();
         sm.abort = 0;
     }
     if (warp == 8) tmem_alloc(&sm.tmem_slot, kTmemCols);
-    if (warp == 9 && lane == 0) {
+    if (warp == 12 && lane == 0) {
         tma_prefetch_desc(&tm_q);
         if constexpr (!k8) {
             tma_prefetch_desc(&tm_k);
@@ -415,16 +394,14 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
     if (work.begin < work.end) {
         Tile t = find_tile<kUnit, kCost>(a, work);
         if (warp < 8) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Split<K>::kSoftmax));
             // ---- softmax of half x --------------------------------------------------
             const int x = warp >> 2, rl = 32 * (warp & 3) + lane;
             const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-            const uint32_t t_s = lanes + T::s(x), t_o = lanes + T::o(x), t_p = lanes + T::p(x);
+            const uint32_t t_o = lanes + T::o(x);
             const float sc = a.scale_log2;
             unsigned n_s = 0;          // units of this half so far
             unsigned unit = 0;         // units of the CTA before this tile
-            Cursor cur;                // K of the current unit; V follows
-            unsigned v_stage = 0;      // V of the unit before
+            Cursor ck, cv;             // K of the current unit; V of the oldest unit not yet released
             bool ok = true;
             while (ok) {
                 const int packed0 = t.t * a.tile, packed = t.q.n * a.group;
@@ -437,121 +414,79 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
                     int g = -100;          // log2 of G
                     for (int u = 0; u < t.n; ++u, ++n_s) {
                         const int key0 = (t.u0 + u) * kUnit;
-                        ok = __all_sync(0xffffffffu, wait(&sm.s_full[x], n_s & 1, sm, a.b.guard));
+                        const uint32_t t_s = lanes + T::s(x, n_s & 1);
+                        ok = __all_sync(0xffffffffu, wait(&sm.s_full[x][n_s & 1], n_s >> 1 & 1, sm, a.b.guard));
                         if (!ok) break;
                         tc_fence_after();
-                        uint32_t s[4][32];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_ld32_async(t_s + 32 * c, s[c]);
-                        const unsigned bad = sm.bad[(unit + u) & 7];
+                        uint32_t s[2][32];
+                        tmem_ld32_async(t_s, s[0]);
+                        tmem_ld32_async(t_s + 32, s[1]);
+                        const unsigned slot = (unit + u) % kLag;
+                        const unsigned bad = sm.bad[slot];
                         if (rl == 0) {
                             // This half is done with the unit's K tile, with the queries after the
-                            // last one, and (S was issued after the last P V had completed) with
-                            // the V tile before.
-                            mbar_arrive(&sm.empty[cur.stage]);
+                            // last one, and (S was issued after that P V had completed) with V of
+                            // the unit two before.
+                            mbar_arrive(&sm.k_empty[ck.stage]);
                             if (u + 1 == t.n) mbar_arrive(&sm.q_empty);
-                            if (kOverlay && u > 0) mbar_arrive(&sm.empty[v_stage]);
+                            if (u > 1) mbar_arrive(&sm.v_empty[cv.stage]);
                         }
-                        cur.next(args.stages);
+                        ck.next(args.k_stages);
+                        if (u > 1) cv.next(args.v_stages);
+                        const uint32_t at = scales + slot * (2 * kUnit * 4);
                         tmem_ld_wait();
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) pin32(s[c]);
-                        if constexpr (!kOverlay) {
-                            tc_fence_before();
-                            mbar_arrive(&sm.s_read[x]);
-                        }
-                        const uint32_t at = scales + ((unit + u) % kScaleUnits) * (2 * kUnit * 4);
+                        pin32(s[0]);
+                        pin32(s[1]);
                         if constexpr (k8) {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) scale_scores(s[c], at + 128 * c);
+                            scale_scores(s[0], at);
+                            scale_scores(s[1], at + 128);
                         }
-                        // With a reference already there, the weights of the first 64
-                        // positions are made against it while the maximum is still being
-                        // taken: it has to move only if some score has outgrown it.
-                        const bool cut = key0 + kUnit - 1 > sure || bad;
-                        const bool ahead = kOverlay && !k8 && u > 0 && !cut && !__any_sync(0xffffffffu, m == -INFINITY);
-                        float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                        float corr = 1.f;
-                        bool moved = false;
-                        const auto settle = [&]() {
-                            const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * sc;
-                            const bool move = top > m + kSlack;
-                            if (move) {
-                                corr = ex2(m - top);
-                                m = top;
-                                l0 *= corr;
-                                l1 *= corr;
-                            }
-                            moved = __any_sync(0xffffffffu, move);
-                        };
-                        if (!ahead) {
-                            if (cut) {
-                                const int last = lim - key0;      // last position of the unit the row sees
+                        if (key0 + kUnit - 1 > sure || bad) {
+                            const int last = lim - key0;      // last position of the unit the row sees
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                if (__any_sync(0xffffffffu, last < 32 * c + 31)) {
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e)
+                                        if (32 * c + e > last) s[c][e] = 0xff800000u;
+                                }
+                            if (bad) {
 #pragma unroll
                                 for (int c = 0; c < 4; ++c)
-                                    if (__any_sync(0xffffffffu, last < 32 * c + 31)) {
+                                    if (bad >> c & 1)
 #pragma unroll
-                                        for (int e = 0; e < 32; ++e)
-                                            if (32 * c + e > last) s[c][e] = 0xff800000u;
-                                    }
-                                if (bad) {
-#pragma unroll
-                                    for (int c = 0; c < 8; ++c)
-                                        if (bad >> c & 1)
-#pragma unroll
-                                            for (int e = 0; e < 16; ++e) s[c / 2][16 * (c % 2) + e] = 0xff800000u;
-                                }
-                            }
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                                for (int e = 0; e < 32; e += 2) top2(v[e / 2 & 3], s[c][e], s[c][e + 1]);
-                            settle();
-#pragma unroll
-                            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                                for (int e = 0; e < 32; e += 2) weigh2(s[c][e], s[c][e + 1], sc, m == -INFINITY ? 0.f : -m);
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                                for (int e = 0; e < 32; e += 2) {
-                                    top2(v[e / 2 & 1], s[c][e], s[c][e + 1]);
-                                    top2(v[2 + (e / 2 & 1)], s[2 + c][e], s[2 + c][e + 1]);
-                                    weigh2(s[c][e], s[c][e + 1], sc, -m);
-                                }
-                            settle();
-                            if (moved) {
-                                // The scores are still in TMEM: P has not been stored yet.
-#pragma unroll
-                                for (int c = 0; c < 2; ++c) tmem_ld32_async(t_s + 32 * c, s[c]);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int c = 0; c < 2; ++c) {
-                                    pin32(s[c]);
-                                    if constexpr (k8) scale_scores(s[c], at + 128 * c);
-#pragma unroll
-                                    for (int e = 0; e < 32; e += 2) weigh2(s[c][e], s[c][e + 1], sc, -m);
-                                }
+                                        for (int e = 0; e < 16; ++e) s[c / 2][16 * (c % 2) + e] = 0xff800000u;
                             }
                         }
-                        bool scale_o = moved;
+                        float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2)
+                                v[e / 2 & 3] = max3(v[e / 2 & 3], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+                        const float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * sc;
+                        // A new reference once the maximum has outgrown the old one.
+                        const bool move = top > m + kSlack;
+                        float corr = 1.f;
+                        if (move) {
+                            corr = ex2(m - top);
+                            m = top;
+                            l0 *= corr;
+                            l1 *= corr;
+                        }
+                        bool scale_o = __any_sync(0xffffffffu, move);
                         if constexpr (k8) {
-                            const int ng = sm.g[(unit + u) % kScaleUnits];
+                            const int ng = sm.g[slot];
                             corr *= pow2i(max(g - ng, -126));
                             scale_o = scale_o || ng != g;
                             g = ng;
                         }
-                        if (u > 0 && (!kOverlay || scale_o)) {
-                            // P V of the unit before: P's columns and O are free after it.
-                            ok = __all_sync(0xffffffffu, wait(&sm.o_full[x], (n_s - 1) & 1, sm, a.b.guard));
+                        if (u > 0 && scale_o) {
+                            // P V of the unit before has to be in O (S of this one came after the one
+                            // before that).
+                            ok = __all_sync(0xffffffffu, wait(&sm.o_full[x][(n_s - 1) & 1], (n_s - 1) >> 1 & 1, sm, a.b.guard));
                             if (!ok) break;
                             tc_fence_after();
-                            if (!kOverlay && rl == 0) mbar_arrive(&sm.empty[v_stage]);
-                        }
-                        v_stage = cur.stage;
-                        cur.next(args.stages);
-                        if (u > 0 && scale_o) {
 #pragma unroll 1
                             for (int c = 0; c < HD / 32; ++c) {
                                 uint32_t o[32];
@@ -564,56 +499,57 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
                             }
                         }
                         const float base = m == -INFINITY ? 0.f : -m;
+                        uint32_t p[32];
+                        [[maybe_unused]] float4 vs;
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            uint32_t p[32];
-                            [[maybe_unused]] float4 vs;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                uint32_t& sy = s[2 * c + e / 16][2 * e % 32];
-                                uint32_t& sz = s[2 * c + e / 16][2 * e % 32 + 1];
-                                if (c) weigh2(sy, sz, sc, base);
-                                float y = __uint_as_float(sy), z = __uint_as_float(sz);
-                                add2(l0, l1, y, z);
-                                if constexpr (k8) {
-                                    if (e % 2 == 0) vs = lds4(at + 4 * kUnit + 4 * (64 * c + 2 * e));
-                                    mul2(y, z, e % 2 ? vs.z : vs.x, e % 2 ? vs.w : vs.y);
-                                }
-                                p[e] = pack2<BF16>(y, z);
+                        for (int e = 0; e < 32; ++e) {
+                            float y = __uint_as_float(s[e / 16][2 * e % 32]), z = __uint_as_float(s[e / 16][2 * e % 32 + 1]);
+                            fma2(y, z, sc, base);
+                            y = ex2(y);
+                            z = ex2(z);
+                            add2(l0, l1, y, z);
+                            if constexpr (k8) {
+                                if (e % 2 == 0) vs = lds4(at + 4 * kUnit + 8 * e);
+                                mul2(y, z, e % 2 ? vs.z : vs.x, e % 2 ? vs.w : vs.y);
                             }
-                            tmem_st32(t_p + 32 * c, p);
-                            tmem_st_wait();
-                            tc_fence_before();
-                            mbar_arrive(c ? &sm.p_hi[x] : &sm.p_lo[x]);
+                            p[e] = pack2<BF16>(y, z);
                         }
+                        tmem_st32(t_s, p);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        mbar_arrive(&sm.p_full[x][n_s & 1]);
                     }
                     if (!ok) break;
                     // ---- the half's rows ------------------------------------------------
-                    ok = __all_sync(0xffffffffu, wait(&sm.o_full[x], (n_s - 1) & 1, sm, a.b.guard));
+                    // The last two P V (S of the last unit came after those before).
+                    ok = t.n < 2 || wait(&sm.o_full[x][n_s & 1], (n_s - 2) >> 1 & 1, sm, a.b.guard);
+                    ok = __all_sync(0xffffffffu, ok && wait(&sm.o_full[x][(n_s - 1) & 1], (n_s - 1) >> 1 & 1, sm, a.b.guard));
                     if (!ok) break;
                     tc_fence_after();
-                    if (rl == 0) mbar_arrive(&sm.empty[v_stage]);
+                    for (int u = max(0, t.n - 2); u < t.n; ++u) {
+                        if (rl == 0) mbar_arrive(&sm.v_empty[cv.stage]);
+                        cv.next(args.v_stages);
+                    }
                     const float l = l0 + l1, unit_g = k8 ? pow2i(g) : 1.f;
                     const PartPlace place = part_place(t);
-                    const int slot = place.slot, r = x * args.sub + rl;
+                    const int r = x * args.sub + rl;
                     // Rows go out through the warp's staging buffer: 64 bytes of each of its 32 rows
                     // at a time, written a row per lane and stored four lanes a row (a row per lane
                     // straight to memory touches 32 lines a store and holds the load / store unit
                     // for 5,000 cycles a tile).
-                    const bool whole = place.whole;
-                    const float f = !whole ? unit_g : l == 0.f ? 0.f : unit_g / l;
+                    const float f = !place.whole ? unit_g : l == 0.f ? 0.f : unit_g / l;
                     char* dst;
-                    if (whole) {
+                    if (place.whole) {
                         const int row = t.q.q0 + i / a.group, qh = t.head * a.group + i % a.group;
                         dst = a.out.data + (long long)row * a.out.row_bytes + (long long)qh * a.out.head_bytes;
                         if (live && a.lse)
                             a.lse[(long long)row * a.n_head + qh] =
                                 l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                     } else {
-                        dst = reinterpret_cast<char*>(a.parts.o + ((long long)slot * a.parts.rows + r) * HD);
+                        dst = reinterpret_cast<char*>(a.parts.o + ((long long)place.slot * a.parts.rows + r) * HD);
                         if (live) {
-                            a.parts.ml[(long long)slot * 2 * a.parts.rows + r] = m;
-                            a.parts.ml[((long long)slot * 2 + 1) * a.parts.rows + r] = l;
+                            a.parts.ml[(long long)place.slot * 2 * a.parts.rows + r] = m;
+                            a.parts.ml[((long long)place.slot * 2 + 1) * a.parts.rows + r] = l;
                         }
                     }
                     if (!live) dst = nullptr;
@@ -624,7 +560,7 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
                         tmem_ld32_async(t_o + 32 * c, o);
                         tmem_ld_wait();
                         pin32(o);
-                        if (whole) {
+                        if (place.whole) {
                             uint32_t w[16];
 #pragma unroll
                             for (int e = 0; e < 16; ++e)
@@ -637,310 +573,317 @@ __global__ void __launch_bounds__(Split<K>::kThreads, 1)
                             put_rows64(stage, reinterpret_cast<const uint32_t(&)[16]>(o[16]), dst, 128 * c + 64, lane);
                         }
                     }
-                    if (!whole && place.begins) {
+                    if (!place.whole && place.begins) {
                         open = true;
                         if (tid == 0) note_open<kCost>(a, work, t);
                     }
                     tc_fence_before();
                 } else {
-                    for (int u = 0; u < 2 * t.n; ++u) cur.next(args.stages);
+                    for (int u = 0; u < t.n; ++u) {
+                        ck.next(args.k_stages);
+                        cv.next(args.v_stages);
+                    }
                 }
                 unit += t.n;
                 next_tile<kUnit, kCost>(a, work, t);
                 if (t.n <= 0) break;
             }
-        } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Split<K>::kOther));
-        }
-        if (warp == 8 || warp == 10) {
-            // ---- products of half x ---------------------------------------------------
+        } else if (warp < 10) {
+            // ---- S of half x ------------------------------------------------------------
             if (lane == 0) {
-                constexpr uint32_t id_s = idesc16(128, kUnit, BF16, false), id_o = idesc16(128, HD, BF16, true);
-                const int x = warp == 8 ? 0 : 1;
-                const uint64_t qd = desc_sw128(q_tiles + x * kTileBytes);
-                const uint32_t t_s = tmem + T::s(x), t_o = tmem + T::o(x), t_p = tmem + T::p(x);
-                unsigned n_u = 0, seg = 0;       // P V products so far; tiles
-                unsigned turns = 0;              // units of tiles with both halves so far
-                Cursor cur;
+                constexpr uint32_t id_s = idesc16(128, kUnit, BF16, false);
+                const int x = warp - 8;
+                const uint64_t qd = desc_sw128(q_tiles + x * kQTile);
+                unsigned n = 0, seg = 0;       // units of the half, tiles
+                Cursor ck;
                 bool ok = true;
-                const auto landed = [&](const Cursor& c) {
-                    ok = ok && wait(&sm.full[c.stage], c.round & 1, sm, a.b.guard);
-                };
-                // S against the K tile at `cur`.
-                const auto issue_s = [&](bool hand_over) {
-                    const uint64_t kd = desc_sw128(ring + cur.stage * kTileBytes);
-#pragma unroll
-                    for (int k = 0; k < HD / 16; ++k) {
-                        if (k == HD / 32 && hand_over) mbar_arrive(&sm.turn[x ^ 1]);
-                        const uint32_t off = (uint32_t)((k / 4) * kHalfBytes + (k % 4) * 32) >> 4;
-                        mma_f16(t_s, qd + off, kd + off, id_s, k != 0 ? 1u : 0u);
-                    }
-                    mma_commit(&sm.s_full[x]);
-                };
                 for (;; ++seg) {
-                    const bool both = t.t * a.tile + args.sub < t.q.n * a.group;
+                    const int halves = t.t * a.tile + args.sub < t.q.n * a.group ? 2 : 1;
+                    if (x == 0) {
+                        if (seg) ok = ok && wait(&sm.q_empty, (seg - 1) & 1, sm, a.b.guard);
+                        if (!ok) break;
+                        mbar_expect_tx(&sm.q_full, (unsigned)(halves * kHalves * args.sub * 128));
+                        for (int h = 0; h < halves; ++h)
+                            for (int c = 0; c < kHalves; ++c)
+                                tma_load_3d(q_tiles + h * kQTile + c * kQBytes, &tm_q, 64 * c, t.head * a.group,
+                                            t.q.q0 + (2 * t.t + h) * args.sub_rows, &sm.q_full);
+                    }
                     ok = ok && wait(&sm.q_full, seg & 1, sm, a.b.guard);
-                    if (x == 1 && !both) {
-                        // No rows in this half: its share of releasing the ring all the same.
-                        for (int e = 0; e < 2 * t.n && ok; ++e) {
-                            landed(cur);
-                            if (ok) mbar_arrive(&sm.empty[cur.stage]);
-                            cur.next(args.stages);
+                    if (x < halves) {
+                        for (int u = 0; u < t.n; ++u, ++n) {
+                            ok = ok && wait(&sm.k_full[ck.stage], ck.round & 1, sm, a.b.guard);
+                            // The buffer's last P, of the unit two before, has been used.
+                            if (n > 1) ok = ok && wait(&sm.o_full[x][n & 1], (n - 2) >> 1 & 1, sm, a.b.guard);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t kd = desc_sw128(k_ring + ck.stage * kTile);
+                            const uint32_t t_s = tmem + T::s(x, n & 1);
+#pragma unroll
+                            for (int k = 0; k < HD / 16; ++k)
+                                mma_f16(t_s, qd + (((k / 4) * kQBytes + (k % 4) * 32) >> 4),
+                                        kd + (((k / 4) * kHalfBytes + (k % 4) * 32) >> 4), id_s, k != 0 ? 1u : 0u);
+                            mma_commit(&sm.s_full[x][n & 1]);
+                            ck.next(args.k_stages);
+                        }
+                    } else {
+                        // No rows in this half: its share of releasing the tiles all the same.
+                        for (int u = 0; u < t.n; ++u) {
+                            ok = ok && wait(&sm.k_full[ck.stage], ck.round & 1, sm, a.b.guard);
+                            if (ok) mbar_arrive(&sm.k_empty[ck.stage]);
+                            ck.next(args.k_stages);
                         }
                         if (ok) mbar_arrive(&sm.q_empty);
-                    } else {
-                        landed(cur);
-                        if (kOverlay && n_u) ok = ok && wait(&sm.o_full[x], (n_u - 1) & 1, sm, a.b.guard);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_s(false);
-                        cur.next(args.stages);
-                        for (int u = 0; u < t.n; ++u) {
-                            const Cursor v = cur;              // V of this unit; K of the next one follows
-                            const bool more = u + 1 < t.n;
-                            cur.next(args.stages);
-                            if (!kOverlay) {
-                                // S of the next unit once this one's is in registers.
-                                ok = ok && wait(&sm.s_read[x], n_u & 1, sm, a.b.guard);
-                                if (more) {
-                                    landed(cur);
-                                    if (!ok) break;
-                                    tc_fence_after();
-                                    issue_s(false);
-                                    cur.next(args.stages);
-                                }
-                            }
-                            landed(v);
-                            const uint64_t vd = desc_mn128(ring + v.stage * kTileBytes);
-                            // The first 64 positions' P V while the others' P is made.
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                ok = ok && wait(c ? &sm.p_hi[x] : &sm.p_lo[x], n_u & 1, sm, a.b.guard);
-                                if (kOverlay && c == 0 && both && (x == 1 || turns))
-                                    ok = ok && wait(&sm.turn[x], (x == 1 ? turns : turns - 1) & 1, sm, a.b.guard);
-                                if (!ok) break;
-                                tc_fence_after();
-#pragma unroll
-                                for (int k = 4 * c; k < 4 * c + 4; ++k)
-                                    mma_ts(t_o, t_p + 8 * k, vd + (2048 * k >> 4), id_o, u > 0 || k > 0 ? 1u : 0u);
-                            }
-                            if (!ok) break;
-                            mma_commit(&sm.o_full[x]);
-                            ++n_u;
-                            if (kOverlay && more) {
-                                landed(cur);
-                                ok = ok && wait(&sm.o_full[x], (n_u - 1) & 1, sm, a.b.guard);
-                                if (!ok) break;
-                                tc_fence_after();
-                                // The other half's turn comes with the second part of S: P V and the
-                                // next S of one half run together, so that the halves' softmaxes fall
-                                // into each other's products.
-                                issue_s(both);
-                                cur.next(args.stages);
-                            }
-                            if (kOverlay && both) {
-                                if (!more) mbar_arrive(&sm.turn[x ^ 1]);
-                                ++turns;
-                            }
-                        }
                     }
                     next_tile<kUnit, kCost>(a, work, t);
                     if (t.n <= 0 || !ok) break;
                 }
-                if (!ok) {   // products in flight end before the tensor memory is given back
+                if (!ok) {   // what is in flight ends before the memory is given back
                     mma_commit(&sm.drain[x]);
                     mbar_wait(&sm.drain[x], 0, kWaitNs);
+                    if (x == 0) mbar_wait(&sm.q_full, seg & 1, kWaitNs);
                 }
             }
             __syncwarp();
-        } else if (warp == 9) {
-            // ---- feed: queries, and 16-bit pages ------------------------------------------
+        } else if (warp < 12) {
+            // ---- P V of half x ------------------------------------------------------------
+            if (lane == 0) {
+                constexpr uint32_t id_o = idesc16(128, HD, BF16, true);
+                const int x = warp - 10;
+                const uint32_t t_o = tmem + T::o(x);
+                unsigned n = 0;
+                Cursor cv;
+                bool ok = true;
+                while (ok) {
+                    const bool rows = x == 0 || t.t * a.tile + args.sub < t.q.n * a.group;
+                    for (int u = 0; u < t.n; ++u) {
+                        ok = ok && wait(&sm.v_full[cv.stage], cv.round & 1, sm, a.b.guard);
+                        if (rows) {
+                            ok = ok && wait(&sm.p_full[x][n & 1], n >> 1 & 1, sm, a.b.guard);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t vd = desc_mn128(v_ring + cv.stage * kTile);
+                            const uint32_t t_p = tmem + T::s(x, n & 1);
+#pragma unroll
+                            for (int k = 0; k < kUnit / 16; ++k)
+                                mma_ts(t_o, t_p + 8 * k, vd + (2048 * k >> 4), id_o, u > 0 || k > 0 ? 1u : 0u);
+                            mma_commit(&sm.o_full[x][n & 1]);
+                            ++n;
+                        } else if (ok) {
+                            mbar_arrive(&sm.v_empty[cv.stage]);
+                        }
+                        cv.next(args.v_stages);
+                    }
+                    next_tile<kUnit, kCost>(a, work, t);
+                    if (t.n <= 0) break;
+                }
+                if (!ok) {
+                    mma_commit(&sm.drain[2 + x]);
+                    mbar_wait(&sm.drain[2 + x], 0, kWaitNs);
+                }
+            }
+            __syncwarp();
+        } else if (!k8 && warp == 12) {
+            // ---- feed: 16-bit pages -------------------------------------------------------
             const int page_rows = 1 << a.kv.page_shift, box = min(page_rows, kUnit), boxes = kUnit / box;
             const int p = lane / kHalves, h = lane % kHalves;
-            unsigned seg = 0, unit = 0, n_tail = 0;
-            Cursor cur;
+            unsigned unit = 0, n_tail = 0;
+            Cursor ck, cv;
             bool ok = true;
-            while (ok) {
-                const int halves = t.t * a.tile + args.sub < t.q.n * a.group ? 2 : 1;
-                if (seg) ok = __all_sync(0xffffffffu, wait(&sm.q_empty, (seg - 1) & 1, sm, a.b.guard));
-                if (!ok) break;
+            // Stores K (kv = 0) or V of unit u of the tile; `ordinal` is the unit's number in the CTA.
+            const auto feed = [&](int u, int kv, unsigned ordinal) {
+                Cursor& cur = kv ? cv : ck;
+                uint64_t* full = kv ? &sm.v_full[cur.stage] : &sm.k_full[cur.stage];
+                uint64_t* empty = kv ? &sm.v_empty[cur.stage] : &sm.k_empty[cur.stage];
+                const int key0 = (t.u0 + u) * kUnit, key = key0 + p * box;
+                int page = -1;
+                bool is_bad = false;
+                if (p < boxes && key < t.keys) {
+                    page = __ldg(a.b.pages + (long long)t.s * a.b.pages_stride + (key >> a.kv.page_shift));
+                    if ((unsigned)page >= (unsigned)a.kv.n_pages) {
+                        is_bad = true;
+                        page = -1;
+                        raise_guard(a.b.guard, QWEN2_GUARD_PAGE);
+                    }
+                }
+                const unsigned bad =
+                    __reduce_or_sync(0xffffffffu, is_bad ? ((1u << (box / 16)) - 1) << (p * box / 16) : 0u);
+                const unsigned bytes = (unsigned)(__popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128);
+                const bool patch = kv && (key0 + kUnit > t.keys || bad);   // positions that are no keys: zeros in V
+                if (cur.round) ok = __all_sync(0xffffffffu, wait(empty, (cur.round - 1) & 1, sm, a.b.guard));
+                if (!ok) return;
+                int at[3];
+                at[args.kv_rank[0]] = key & (page_rows - 1);
+                at[args.kv_rank[1]] = t.head;
+                at[args.kv_rank[2]] = page;
+                const uint32_t tile = (kv ? v_ring : k_ring) + cur.stage * kTile;
+                uint64_t* bar = patch ? &sm.tail : full;
                 if (lane == 0) {
-                    mbar_expect_tx(&sm.q_full, (unsigned)(halves * kHalves * args.sub * 128));
-                    for (int x = 0; x < halves; ++x)
-                        for (int c = 0; c < kHalves; ++c)
-                            tma_load_3d(q_tiles + x * kTileBytes + c * kHalfBytes, &tm_q, 64 * c, t.head * a.group,
-                                        t.q.q0 + (2 * t.t + x) * args.sub_rows, &sm.q_full);
+                    if (!kv) sm.bad[ordinal % kLag] = bad;
+                    mbar_expect_tx(bar, bytes);
                 }
                 __syncwarp();
-                ++seg;
-                for (int u = 0; !k8 && u < t.n && ok; ++u, ++unit) {
-                    const int key0 = (t.u0 + u) * kUnit, key = key0 + p * box;
-                    int page = -1;
-                    bool is_bad = false;
-                    if (p < boxes && key < t.keys) {
-                        page = __ldg(a.b.pages + (long long)t.s * a.b.pages_stride + (key >> a.kv.page_shift));
-                        if ((unsigned)page >= (unsigned)a.kv.n_pages) {
-                            is_bad = true;
-                            page = -1;
-                            raise_guard(a.b.guard, QWEN2_GUARD_PAGE);
-                        }
-                    }
-                    const unsigned bad = __reduce_or_sync(
-                        0xffffffffu, is_bad ? ((1u << (box / 16)) - 1) << (p * box / 16) : 0u);
-                    const unsigned bytes = (unsigned)(__popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128);
-                    const bool whole = key0 + kUnit <= t.keys && !bad;
-                    int at[3];
-                    at[args.kv_rank[0]] = key & (page_rows - 1);
-                    at[args.kv_rank[1]] = t.head;
-                    at[args.kv_rank[2]] = page;
-                    for (int kv = 0; kv < 2 && ok; ++kv, cur.next(args.stages)) {
-                        const unsigned st = cur.stage, round = cur.round;
-                        if (round) ok = __all_sync(0xffffffffu, wait(&sm.empty[st], (round - 1) & 1, sm, a.b.guard));
-                        if (!ok) break;
-                        const uint32_t tile = ring + st * kTileBytes;
-                        uint64_t* bar = kv && !whole ? &sm.tail : &sm.full[st];
-                        if (lane == 0) {
-                            if (!kv) sm.bad[unit & 7] = bad;
-                            mbar_expect_tx(bar, bytes);
-                        }
-                        __syncwarp();
-                        if (page >= 0)
-                            tma_load_4d(tile + h * kHalfBytes + p * box * 128, kv ? &tm_v : &tm_k, 64 * h, at[0], at[1],
-                                        at[2], bar);
-                        if (kv && !whole) {
-                            // Positions that are no keys: zeros in V.
-                            ok = __all_sync(0xffffffffu, wait(&sm.tail, n_tail & 1, sm, a.b.guard));
-                            ++n_tail;
-                            if (!ok) {
-                                mbar_wait(&sm.tail, (n_tail - 1) & 1, kWaitNs);
-                                break;
-                            }
-                            // Eight lanes a 128-byte row, four rows a store.
-                            for (int r = (bad ? 0 : max(0, t.keys - key0) & ~3) + (lane >> 3); r < kUnit; r += 4)
-                                if (key0 + r >= t.keys || (bad >> (r / 16) & 1))
+                if (page >= 0)
+                    tma_load_4d(tile + h * kHalfBytes + p * box * 128, kv ? &tm_v : &tm_k, 64 * h, at[0], at[1], at[2], bar);
+                cur.next(kv ? args.v_stages : args.k_stages);
+                if (patch) {
+                    ok = __all_sync(0xffffffffu, wait(&sm.tail, n_tail & 1, sm, a.b.guard));
+                    if (!ok) mbar_wait(&sm.tail, n_tail & 1, kWaitNs);
+                    ++n_tail;
+                    // Eight lanes a 128-byte row, four rows a store.
+                    for (int r = (bad ? 0 : max(0, t.keys - key0) & ~3) + (lane >> 3); r < kUnit; r += 4)
+                        if (key0 + r >= t.keys || (bad >> (r / 16) & 1))
 #pragma unroll
-                                    for (int c = 0; c < kHalves; ++c)
-                                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                                         tile + c * kHalfBytes + r * 128 + (lane & 7) * 16),
-                                                     "r"(0)
-                                                     : "memory");
-                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&sm.full[st]);
-                        }
-                    }
+                            for (int c = 0; c < kHalves; ++c)
+                                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                                 tile + c * kHalfBytes + r * 128 + (lane & 7) * 16),
+                                             "r"(0)
+                                             : "memory");
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full);
                 }
+            };
+            while (ok) {
+                feed(0, 0, unit);
+                for (int u = 0; u < t.n && ok; ++u) {
+                    if (u + 1 < t.n) feed(u + 1, 0, unit + u + 1);
+                    if (ok) feed(u, 1, unit + u);
+                }
+                unit += t.n;
                 next_tile<kUnit, kCost>(a, work, t);
-                if (t.n <= 0 || !ok) break;
+                if (t.n <= 0) break;
             }
-            if (!ok && !k8) {   // copies in flight land before the shared memory is given back
-                for (unsigned st = 0; st < (unsigned)args.stages; ++st)   // each stage's last entry
-                    if (st < cur.stage || cur.round)
-                        mbar_wait(&sm.full[st], (st < cur.stage ? cur.round : cur.round - 1) & 1, kWaitNs);
-            }
-            if (!ok) {
-                if (seg) mbar_wait(&sm.q_full, (seg - 1) & 1, kWaitNs);
+            if (!ok) {   // copies in flight land before the shared memory is given back
+                for (int i = 0; i < kMaxStages; ++i) {   // each stage's last entry
+                    if (i < ck.stage || (ck.round && i < args.k_stages))
+                        mbar_wait(&sm.k_full[i], (i < ck.stage ? ck.round : ck.round - 1) & 1, kWaitNs);
+                    if (i < cv.stage || (cv.round && i < args.v_stages))
+                        mbar_wait(&sm.v_full[i], (i < cv.stage ? cv.round : cv.round - 1) & 1, kWaitNs);
+                }
             }
             __syncwarp();
         } else if (k8 && warp >= 12) {
             // ---- feed: 8-bit pages ------------------------------------------------------
-            // Thread e takes 16-byte piece e % 4 of row e / 4 (+ 32 rows a step) of
-            // each 64-dim half: two adjacent rows' pieces fill all banks.
+            // Thread e takes 16-byte piece e % 4 of row e / 4 (+ 32) of each 64-dim half:
+            // two adjacent rows' pieces fill all banks.
             const int e0 = tid - 384, piece = e0 & 3, row0 = e0 >> 2;
-            constexpr int kPieces = 4 * kHalves;        // per thread and tile
+            constexpr int kPieces = 2 * kHalves;        // per thread and tile
             unsigned unit = 0;
-            Cursor cur;
-            bool ok = true, stop = false;
-            while (!stop) {
-                int g = -100;
-                for (int u = 0; u < t.n; ++u, ++unit) {
-                    const int key0 = (t.u0 + u) * kUnit;
-                    // Lane l holds the page of positions 16 (l % 8) .. of the unit.
-                    const int key_l = key0 + 16 * (lane & 7);
-                    int page_l = -1;
-                    bool is_bad = false;
-                    if (key_l < t.keys) {
-                        page_l = __ldg(a.b.pages + (long long)t.s * a.b.pages_stride + (key_l >> a.kv.page_shift));
-                        if ((unsigned)page_l >= (unsigned)a.kv.n_pages) {
-                            is_bad = true;
-                            page_l = -1;
-                            raise_guard(a.b.guard, QWEN2_GUARD_PAGE);
-                        }
-                    }
-                    const unsigned bad = __ballot_sync(0xffffffffu, is_bad) & 0xffu;
-                    // This thread's rows: row0 + 32 j, j = 0 .. 3.
-                    long long src[4];
-                    bool in[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int r = row0 + 32 * j, pg = __shfl_sync(0xffffffffu, page_l, r >> 4);
-                        in[j] = pg >= 0 && key0 + r < t.keys;
-                        src[j] = in[j] ? (long long)pg * a.kv.page_bytes +
-                                             (long long)((key0 + r) & ((1 << a.kv.page_shift) - 1)) * a.kv.token_bytes +
-                                             (long long)t.head * a.kv.head_bytes + 16 * piece
-                                       : 0;
-                    }
-                    // Position e0's scales.
-                    const int pg_s = __shfl_sync(0xffffffffu, page_l, (e0 >> 4) & 7);
-                    float ks = 0.f, vs = 0.f;
-                    if (pg_s >= 0 && key0 + e0 < t.keys) {
-                        const long long i = (((long long)pg_s * a.kv.n_kv + t.head) << a.kv.page_shift) +
-                                            ((key0 + e0) & ((1 << a.kv.page_shift) - 1));
-                        ks = __ldg(a.kv.k_scale + i);
-                        vs = __ldg(a.kv.v_scale + i);
-                    }
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const char* base = kv ? a.kv.v : a.kv.k;
-                        uint4 raw[kPieces];
-#pragma unroll
-                        for (int i = 0; i < kPieces; ++i)
-                            raw[i] = in[i & 3] ? ld_stream_v4(base + src[i & 3] + 64 * (i >> 2))
-                                               : make_uint4(0, 0, 0, 0);
-                        const unsigned st = cur.stage, round = cur.round;
-                        if (round && ok) ok = __all_sync(0xffffffffu, wait(&sm.empty[st], (round - 1) & 1, sm, a.b.guard));
-                        if (kv == 0) {
-                            // The slot of this unit's scales is free: with at most 6 stages the V tile stored last took
-                            // the place of one whose P V had completed, of the unit kScaleUnits back or a later one.
-                            const unsigned slot = unit % kScaleUnits;
-                            // The largest v scale of the unit, over the four warps.
-                            float top = warp_max(vs);
-                            float* red = reinterpret_cast<float*>(&sm) + (kHead - 64) / 4 + 4 * (unit & 1);
-                            if (lane == 0) red[warp & 3] = top;
-                            stop = !feeders_agree(ok);
-                            if (stop) break;
-                            top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-                            g = max(g, ceil_log2(top));
-                            const uint32_t at = scales + slot * (2 * kUnit * 4) + 4 * e0;
-                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(ks) : "memory");
-                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * kUnit), "f"(vs * pow2i(-g)) : "memory");
-                            if (e0 == 0) {
-                                sm.g[slot] = g;
-                                sm.bad[unit & 7] = (bad & 0xffu);
-                            }
-                        }
-                        if (!ok) break;     // the others learn of it at the next unit's barrier
-                        const uint32_t tile = ring + st * kTileBytes;
-#pragma unroll
-                        for (int i = 0; i < kPieces; ++i) {
-                            uint32_t o[8];
-                            widen16<K, BF16>(raw[i], o);
-                            const int r = row0 + 32 * (i & 3);
-                            const uint32_t at = tile + (i >> 2) * kHalfBytes + r * 128;
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                                 at + (((2 * piece + j) ^ (r & 7)) << 4)),
-                                             "r"(o[4 * j]), "r"(o[4 * j + 1]), "r"(o[4 * j + 2]), "r"(o[4 * j + 3])
-                                             : "memory");
-                        }
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.full[st]);
-                        cur.next(args.stages);
-                    }
-                    if (stop) break;
+            Cursor ck, cv;
+            bool ok = true;
+            int g = -100;
+            // The codes of K or V of a unit on their way, and for K the scales of its positions
+            // lane and lane + 32 (every warp has all of them, and so the same G).
+            struct Load {
+                uint4 raw[kPieces];
+                float ks[2], vs[2];
+                unsigned bad;
+            };
+            // Lane l's page of positions 16 (l % 4) .. of a unit: -1 for none (as read: it is
+            // checked when it is used, a turn later).
+            const auto look_up = [&](int u) {
+                const int key = (t.u0 + u) * kUnit + 16 * (lane & 3);
+                if (u >= t.n || key >= t.keys) return -1;
+                return __ldg(a.b.pages + (long long)t.s * a.b.pages_stride + (key >> a.kv.page_shift));
+            };
+            const auto load = [&](int u, int kv, int page_l, Load& ld) {
+                const int key0 = (t.u0 + u) * kUnit, mask = (1 << a.kv.page_shift) - 1;
+                const bool there = key0 + 16 * (lane & 3) < t.keys;
+                if ((unsigned)page_l >= (unsigned)a.kv.n_pages) page_l = -1;
+                if (!kv) {
+                    ld.bad = __ballot_sync(0xffffffffu, there && page_l < 0) & 0xfu;
+                    if (ld.bad && lane == 0) raise_guard(a.b.guard, QWEN2_GUARD_PAGE);
                 }
+                const char* base = kv ? a.kv.v : a.kv.k;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = row0 + 32 * j, pg = __shfl_sync(0xffffffffu, page_l, r >> 4);
+                    const bool in = pg >= 0 && key0 + r < t.keys;
+                    const char* src = base + (in ? (long long)pg * a.kv.page_bytes +
+                                                       (long long)((key0 + r) & mask) * a.kv.token_bytes +
+                                                       (long long)t.head * a.kv.head_bytes
+                                                 : 0) + 16 * piece;
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h)
+                        ld.raw[2 * h + j] = in ? ld_stream_v4(src + 64 * h) : make_uint4(0, 0, 0, 0);
+                }
+                if (!kv) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int r = lane + 32 * j, pg = __shfl_sync(0xffffffffu, page_l, r >> 4);
+                        ld.ks[j] = ld.vs[j] = 0.f;
+                        if (pg >= 0 && key0 + r < t.keys) {
+                            const long long i = (((long long)pg * a.kv.n_kv + t.head) << a.kv.page_shift) + ((key0 + r) & mask);
+                            ld.ks[j] = __ldg(a.kv.k_scale + i);
+                            ld.vs[j] = __ldg(a.kv.v_scale + i);
+                        }
+                    }
+                }
+            };
+            const auto store = [&](int kv, unsigned ordinal, const Load& ld) {
+                Cursor& cur = kv ? cv : ck;
+                if (cur.round)
+                    ok = __all_sync(0xffffffffu, ok && wait(kv ? &sm.v_empty[cur.stage] : &sm.k_empty[cur.stage],
+                                                            (cur.round - 1) & 1, sm, a.b.guard));
+                if (!ok) return;
+                if (!kv) {
+                    const unsigned slot = ordinal % kLag;
+                    g = max(g, ceil_log2(warp_max(fmaxf(ld.vs[0], ld.vs[1]))));
+                    if (warp == 12) {
+                        const float down = pow2i(-g);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t at = scales + slot * (2 * kUnit * 4) + 4 * (lane + 32 * j);
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(ld.ks[j]) : "memory");
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * kUnit), "f"(ld.vs[j] * down) : "memory");
+                        }
+                        if (lane == 0) {
+                            sm.g[slot] = g;
+                            sm.bad[slot] = ld.bad;
+                        }
+                    }
+                }
+                const uint32_t tile = (kv ? v_ring : k_ring) + cur.stage * kTile;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    uint32_t o[8];
+                    widen16<K, BF16>(ld.raw[i], o);
+                    const int r = row0 + 32 * (i & 1);
+                    const uint32_t at = tile + (i >> 1) * kHalfBytes + r * 128;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         at + (((2 * piece + j) ^ (r & 7)) << 4)),
+                                     "r"(o[4 * j]), "r"(o[4 * j + 1]), "r"(o[4 * j + 2]), "r"(o[4 * j + 3])
+                                     : "memory");
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(kv ? &sm.v_full[cur.stage] : &sm.k_full[cur.stage]);
+                cur.next(kv ? args.v_stages : args.k_stages);
+            };
+            while (ok) {
+                g = -100;
+                // K of a unit is stored a unit before V.  The codes stored in a turn were asked for
+                // in the turn before, their pages in the one before that.
+                Load k[2], v[2];
+                int page0 = look_up(0), page1 = look_up(1), page2;    // of units u, u + 1, u + 2 below
+                load(0, 0, page0, k[0]);
+                if (t.n > 1) load(1, 0, page1, k[1]);
+                load(0, 1, page0, v[0]);
+                page2 = look_up(2);
+                store(0, unit, k[0]);
+#pragma unroll 2
+                for (int u = 0; u < t.n && ok; ++u) {
+                    const int page3 = look_up(u + 3);
+                    if (u + 2 < t.n) load(u + 2, 0, page2, k[u & 1]);
+                    if (u + 1 < t.n) load(u + 1, 1, page1, v[(u + 1) & 1]);
+                    if (u + 1 < t.n) store(0, unit + u + 1, k[(u + 1) & 1]);
+                    if (ok) store(1, unit + u, v[u & 1]);
+                    page1 = page2;
+                    page2 = page3;
+                }
+                unit += t.n;
                 next_tile<kUnit, kCost>(a, work, t);
                 if (t.n <= 0) break;
             }
@@ -1008,14 +951,15 @@ bool encode_q(CUtensorMap* m, const Rows& q, int n_rows, int n_head, int group, 
 template <int HD, bool BF16, Kind K>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, TcArgs& args, int n_sm,
                    bool chained, cudaStream_t st) {
-    constexpr int kTileBytes = HD / 64 * kHalfBytes, kThreads = Split<K>::kThreads;
+    constexpr int kQTile = HD / 64 * kQBytes, kTile = HD / 64 * kHalfBytes, kThreads = kThreadsOf<K>;
     auto kern = k_paged_attn_tc<HD, BF16, K>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
-    const int rest = kStaging + 8 * (args.a.b.n_seq + 1) + (K == kSame16 ? 0 : kScaleUnits * 2 * kUnit * 4);
-    const int room = 227 * 1024 - 1024 - kHead - rest - 2 * kTileBytes;
-    args.stages = min(K == kSame16 ? kMaxStages : kMaxStages8, room / kTileBytes);
-    const size_t smem = 1024 + kHead + (size_t)(2 + args.stages) * kTileBytes + rest;
+    const int rest = kStaging + 8 * (args.a.b.n_seq + 1) + (K == kSame16 ? 0 : kLag * 2 * kUnit * 4);
+    const int tiles = (227 * 1024 - 1024 - kHead - rest - 2 * kQTile) / kTile;
+    args.k_stages = min(kMaxStages, tiles / 2);
+    args.v_stages = min(kMaxStages, tiles - args.k_stages);
+    const size_t smem = 1024 + kHead + 2 * kQTile + (size_t)(args.k_stages + args.v_stages) * kTile + rest;
     if (chained) return launch_pdl(kern, dim3(n_sm), dim3(kThreads), smem, st, q, k, v, args);
     kern<<<n_sm, kThreads, smem, st>>>(q, k, v, args);
     return cudaGetLastError();
@@ -1054,7 +998,7 @@ cudaError_t enqueue_attention_tc(const TcMaps& m, const AttnArgs& a, int format,
     args.sub = a.tile / 2;
     args.sub_rows = args.sub / a.group;
     for (int i = 0; i < 3; ++i) args.kv_rank[i] = m.kv_rank[i];
-    args.min_slots = kCost + 2;
+    args.min_slots = kCost + 4;
     if (format == QWEN2_KV_INT8) return launch_hd<kInt8>(m, args, head_dim, bf16, n_sm, chained, st);
     if (format == QWEN2_KV_E4M3) return launch_hd<kE4m3>(m, args, head_dim, bf16, n_sm, chained, st);
     return launch_hd<kSame16>(m, args, head_dim, bf16, n_sm, chained, st);
