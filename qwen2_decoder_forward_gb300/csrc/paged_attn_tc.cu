@@ -26,18 +26,21 @@
 // of 128 positions, with S behind P V, left the tensor pipe idle half the
 // time: softmax, P V, S and three hand-overs of 200 to 300 cycles in a row.)
 //
-// Warps: 0-3 softmax of A, 4-7 of B; 8 and 9 issue S of A and B (8 also asks
-// for the queries), 10 and 11 P V (each wait or commit costs an issuing thread
-// 100 to 150 cycles and S of a unit waits for P V of an earlier one: one thread
-// for both products of a half took 2,160 cycles a unit, half of them waits).
-// Warp 12 feeds K and V.  TMEM (512 columns): S at 128 x + 64 b for buffer b of
-// half x, O from 256.
+// Warps: 0-3 softmax of A, 4-7 of B; 8 issues S of both (and asks for the
+// queries), 9 P V of both; 10 loads pages.  S and P V have a thread each, since
+// S of a unit waits for P V of an earlier one and every wait or commit costs
+// the issuing thread 100 to 150 cycles (one thread for all of a half's products
+// took 2,160 cycles a unit, half of them waits).  TMEM (512 columns): S at
+// 128 x + 64 b for buffer b of half x, O from 256.
 //
-// 8-bit pages: four warps (12-15) read the codes, widen them to exact
-// 16-bit values (of the queries' type) and store the swizzled tiles that TMA
-// would have written.  The scales stay out of the products: k's multiplies the
-// scores, v's the probabilities, relative to G, the largest v scale so far
-// rounded up to a power of two, which O carries like the reference m.
+// 8-bit pages: TMA brings codes and scales into a ring of their own, and four
+// more warps (12-15) widen the codes to exact 16-bit values (of the queries'
+// type) in the swizzled tiles that TMA would have written (loading them
+// through registers ran at a third of the speed: a page id, codes and scales
+// in flight share a warp's few load counters, and each wait for one was a wait
+// for all).  The scales stay out of the products: k's multiplies the scores,
+// v's the probabilities, relative to G, the largest v scale so far rounded up
+// to a power of two, which O carries like the reference m.
 //
 // V is the [position][dim] tile as it lies in the pages: an MN-major B
 // operand, so nothing is transposed.  Positions of the last unit that are no
@@ -62,12 +65,17 @@ constexpr int kCost = 4;                   // slots of a tile beside its units (
 enum Kind { kSame16, kInt8, kE4m3 };
 constexpr int kFeeders = 4;                // warps that widen 8-bit codes
 template <Kind K>
-constexpr int kThreadsOf = K == kSame16 ? 416 : 512;
+constexpr int kThreadsOf = K == kSame16 ? 352 : 512;
 constexpr int kStaging = 8 * 2048;         // output rows on their way, 2 KB per softmax warp
-constexpr int kLag = 8;                    // units whose scales and bad pages are kept
-constexpr int kMaxStages = 6;              // K tiles, and V tiles, in the ring: at most kLag - 2, so that a unit's
-                                           // slot is free when its K is stored: the V stored just before, of the
-                                           // unit two back, took the place of one whose P V had completed
+constexpr int kLag = 8;                    // units whose scales are kept
+constexpr int kBadLag = 16;                // units whose bad pages are kept: they are noted earlier
+constexpr int kMaxStages = 6;              // K tiles, and V tiles, in the ring.  At most kLag - 2, so that the slot
+                                           // of a unit's scales is free when its K is stored: the V stored just
+                                           // before, of the unit two back, took the place of one whose P V had
+                                           // completed.
+constexpr int kTiles8 = 3;                 // 8-bit pages: K tiles, and V tiles
+constexpr int kMaxRaw = 6;                 // 8-bit pages: tiles of codes; kMaxRaw / 2 + 2 + kTiles8 <= kBadLag
+constexpr int kRawScales = 2 * kUnit * 4;  // k's and v's scales behind each tile of codes
 constexpr int kQBytes = 128 * 128;         // 128 rows of 64 16-bit elements
 constexpr int kHalfBytes = kUnit * 128;    // 64 positions of 64 16-bit elements
 constexpr uint32_t kTmemCols = 512;
@@ -78,8 +86,9 @@ constexpr float kSlack = 8.f;              // log2 of the growth that is left in
 // parity wait can tell only the current phase from the one before it.
 struct TcSmem {
     uint64_t k_full[kMaxStages], k_empty[kMaxStages], v_full[kMaxStages], v_empty[kMaxStages];
-    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_full[2][2], tail, drain[4];
-    unsigned bad[kLag];                    // per unit (mod kLag): its positions in bad pages, 16 per bit
+    uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
+    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], o_full[2][2], tail, drain[2];
+    unsigned bad[kBadLag];                 // per unit (mod kBadLag): its positions in bad pages, 16 per bit
     int g[kLag];                           // 8-bit pages, per unit: log2 of G
     uint32_t tmem_slot;
     int abort;
@@ -91,7 +100,7 @@ struct TcArgs {
     AttnArgs a;
     int sub;              // packed rows of a half: R * group
     int sub_rows;         // R
-    int k_stages, v_stages;
+    int k_stages, v_stages, raw_stages;
     int kv_rank[3];       // tensor-map dims (1..3) of position, head, page
     int min_slots;
 };
@@ -131,6 +140,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, 
         "%5}], [%6];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
         : "memory");
+}
+
+// Untiled copy of `bytes` (a multiple of 16, both ends 16-byte aligned).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, int bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
 }
 
 // Descriptor of a V tile as B operand with N = dims contiguous (MN-major,
@@ -348,10 +364,12 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
     const uint32_t q_tiles = smem_addr(&sm) + kHead;                 // A, B
     const uint32_t k_ring = q_tiles + 2 * kQTile, v_ring = k_ring + args.k_stages * kTile;
     const uint32_t staging = v_ring + args.v_stages * kTile;
-    const uint32_t scales = staging + kStaging;                      // 8-bit: [kLag][k, v / G][kUnit] f32
+    // 8-bit pages: tiles of codes [64-dim half][kUnit][64 bytes] and their scales, then [kLag][k, v / G][kUnit] f32.
+    constexpr int kRaw = kHalves * kUnit * 64 + kRawScales;
+    const uint32_t raw_ring = staging + kStaging, scales = raw_ring + args.raw_stages * kRaw;
     long long* prefix = reinterpret_cast<long long*>(tc_smem_raw + pad + kHead + 2 * kQTile +
                                                      (args.k_stages + args.v_stages) * kTile + kStaging +
-                                                     (k8 ? kLag * 2 * kUnit * 4 : 0));
+                                                     (k8 ? args.raw_stages * kRaw + kLag * 2 * kUnit * 4 : 0));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_launch_dependents();
@@ -361,6 +379,10 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
             mbar_init(&sm.v_full[i], k8 ? kFeeders : 1);
             mbar_init(&sm.k_empty[i], 2);
             mbar_init(&sm.v_empty[i], 2);
+        }
+        for (int i = 0; i < kMaxRaw; ++i) {
+            mbar_init(&sm.raw_full[i], 1);
+            mbar_init(&sm.raw_empty[i], kFeeders);
         }
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_empty, 2);
@@ -372,18 +394,16 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
             mbar_init(&sm.o_full[x][0], 1);
             mbar_init(&sm.o_full[x][1], 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&sm.drain[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&sm.drain[i], 1);
         mbar_init(&sm.tail, 1);
         mbar_init_fence();
         sm.abort = 0;
     }
     if (warp == 8) tmem_alloc(&sm.tmem_slot, kTmemCols);
-    if (warp == 12 && lane == 0) {
+    if (warp == 10 && lane == 0) {
         tma_prefetch_desc(&tm_q);
-        if constexpr (!k8) {
-            tma_prefetch_desc(&tm_k);
-            tma_prefetch_desc(&tm_v);
-        }
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
     }
     const WorkList work = build_work<kUnit, kCost>(a, prefix, args.min_slots);
     tc_fence_before();
@@ -422,7 +442,7 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                         tmem_ld32_async(t_s, s[0]);
                         tmem_ld32_async(t_s + 32, s[1]);
                         const unsigned slot = (unit + u) % kLag;
-                        const unsigned bad = sm.bad[slot];
+                        const unsigned bad = sm.bad[(unit + u) % kBadLag];
                         if (rl == 0) {
                             // This half is done with the unit's K tile, with the queries after the
                             // last one, and (S was issued after that P V had completed) with V of
@@ -588,88 +608,88 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                 next_tile<kUnit, kCost>(a, work, t);
                 if (t.n <= 0) break;
             }
-        } else if (warp < 10) {
-            // ---- S of half x ------------------------------------------------------------
+        } else if (warp == 8) {
+            // ---- queries, and S of both halves ----------------------------------------------
             if (lane == 0) {
                 constexpr uint32_t id_s = idesc16(128, kUnit, BF16, false);
-                const int x = warp - 8;
-                const uint64_t qd = desc_sw128(q_tiles + x * kQTile);
-                unsigned n = 0, seg = 0;       // units of the half, tiles
+                unsigned n[2] = {0, 0}, seg = 0;       // units of each half, tiles
                 Cursor ck;
                 bool ok = true;
                 for (;; ++seg) {
                     const int halves = t.t * a.tile + args.sub < t.q.n * a.group ? 2 : 1;
-                    if (x == 0) {
-                        if (seg) ok = ok && wait(&sm.q_empty, (seg - 1) & 1, sm, a.b.guard);
-                        if (!ok) break;
-                        mbar_expect_tx(&sm.q_full, (unsigned)(halves * kHalves * args.sub * 128));
-                        for (int h = 0; h < halves; ++h)
-                            for (int c = 0; c < kHalves; ++c)
-                                tma_load_3d(q_tiles + h * kQTile + c * kQBytes, &tm_q, 64 * c, t.head * a.group,
-                                            t.q.q0 + (2 * t.t + h) * args.sub_rows, &sm.q_full);
-                    }
-                    ok = ok && wait(&sm.q_full, seg & 1, sm, a.b.guard);
-                    if (x < halves) {
-                        for (int u = 0; u < t.n; ++u, ++n) {
-                            ok = ok && wait(&sm.k_full[ck.stage], ck.round & 1, sm, a.b.guard);
+                    if (seg) ok = wait(&sm.q_empty, (seg - 1) & 1, sm, a.b.guard);
+                    if (!ok) break;
+                    mbar_expect_tx(&sm.q_full, (unsigned)(halves * kHalves * args.sub * 128));
+                    for (int x = 0; x < halves; ++x)
+                        for (int c = 0; c < kHalves; ++c)
+                            tma_load_3d(q_tiles + x * kQTile + c * kQBytes, &tm_q, 64 * c, t.head * a.group,
+                                        t.q.q0 + (2 * t.t + x) * args.sub_rows, &sm.q_full);
+                    ok = wait(&sm.q_full, seg & 1, sm, a.b.guard);
+                    for (int u = 0; u < t.n && ok; ++u) {
+                        ok = wait(&sm.k_full[ck.stage], ck.round & 1, sm, a.b.guard);
+                        const uint64_t kd = desc_sw128(k_ring + ck.stage * kTile);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            if (x >= halves) {
+                                // No rows in this half: its share of releasing the tile all the same.
+                                if (ok) mbar_arrive(&sm.k_empty[ck.stage]);
+                                continue;
+                            }
                             // The buffer's last P, of the unit two before, has been used.
-                            if (n > 1) ok = ok && wait(&sm.o_full[x][n & 1], (n - 2) >> 1 & 1, sm, a.b.guard);
+                            const unsigned b = n[x] & 1;
+                            if (n[x] > 1) ok = ok && wait(&sm.o_full[x][b], (n[x] - 2) >> 1 & 1, sm, a.b.guard);
                             if (!ok) break;
                             tc_fence_after();
-                            const uint64_t kd = desc_sw128(k_ring + ck.stage * kTile);
-                            const uint32_t t_s = tmem + T::s(x, n & 1);
+                            const uint64_t qd = desc_sw128(q_tiles + x * kQTile);
+                            const uint32_t t_s = tmem + T::s(x, b);
 #pragma unroll
                             for (int k = 0; k < HD / 16; ++k)
                                 mma_f16(t_s, qd + (((k / 4) * kQBytes + (k % 4) * 32) >> 4),
                                         kd + (((k / 4) * kHalfBytes + (k % 4) * 32) >> 4), id_s, k != 0 ? 1u : 0u);
-                            mma_commit(&sm.s_full[x][n & 1]);
-                            ck.next(args.k_stages);
+                            mma_commit(&sm.s_full[x][b]);
+                            ++n[x];
                         }
-                    } else {
-                        // No rows in this half: its share of releasing the tiles all the same.
-                        for (int u = 0; u < t.n; ++u) {
-                            ok = ok && wait(&sm.k_full[ck.stage], ck.round & 1, sm, a.b.guard);
-                            if (ok) mbar_arrive(&sm.k_empty[ck.stage]);
-                            ck.next(args.k_stages);
-                        }
-                        if (ok) mbar_arrive(&sm.q_empty);
+                        ck.next(args.k_stages);
                     }
+                    if (ok && halves == 1) mbar_arrive(&sm.q_empty);
                     next_tile<kUnit, kCost>(a, work, t);
                     if (t.n <= 0 || !ok) break;
                 }
                 if (!ok) {   // what is in flight ends before the memory is given back
-                    mma_commit(&sm.drain[x]);
-                    mbar_wait(&sm.drain[x], 0, kWaitNs);
-                    if (x == 0) mbar_wait(&sm.q_full, seg & 1, kWaitNs);
+                    mma_commit(&sm.drain[0]);
+                    mbar_wait(&sm.drain[0], 0, kWaitNs);
+                    mbar_wait(&sm.q_full, seg & 1, kWaitNs);
                 }
             }
             __syncwarp();
-        } else if (warp < 12) {
-            // ---- P V of half x ------------------------------------------------------------
+        } else if (warp == 9) {
+            // ---- P V of both halves -----------------------------------------------------------
             if (lane == 0) {
                 constexpr uint32_t id_o = idesc16(128, HD, BF16, true);
-                const int x = warp - 10;
-                const uint32_t t_o = tmem + T::o(x);
-                unsigned n = 0;
+                unsigned n[2] = {0, 0};
                 Cursor cv;
                 bool ok = true;
                 while (ok) {
-                    const bool rows = x == 0 || t.t * a.tile + args.sub < t.q.n * a.group;
-                    for (int u = 0; u < t.n; ++u) {
-                        ok = ok && wait(&sm.v_full[cv.stage], cv.round & 1, sm, a.b.guard);
-                        if (rows) {
-                            ok = ok && wait(&sm.p_full[x][n & 1], n >> 1 & 1, sm, a.b.guard);
+                    const int halves = t.t * a.tile + args.sub < t.q.n * a.group ? 2 : 1;
+                    for (int u = 0; u < t.n && ok; ++u) {
+                        ok = wait(&sm.v_full[cv.stage], cv.round & 1, sm, a.b.guard);
+                        const uint64_t vd = desc_mn128(v_ring + cv.stage * kTile);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            if (x >= halves) {
+                                if (ok) mbar_arrive(&sm.v_empty[cv.stage]);
+                                continue;
+                            }
+                            const unsigned b = n[x] & 1;
+                            ok = ok && wait(&sm.p_full[x][b], n[x] >> 1 & 1, sm, a.b.guard);
                             if (!ok) break;
                             tc_fence_after();
-                            const uint64_t vd = desc_mn128(v_ring + cv.stage * kTile);
-                            const uint32_t t_p = tmem + T::s(x, n & 1);
 #pragma unroll
                             for (int k = 0; k < kUnit / 16; ++k)
-                                mma_ts(t_o, t_p + 8 * k, vd + (2048 * k >> 4), id_o, u > 0 || k > 0 ? 1u : 0u);
-                            mma_commit(&sm.o_full[x][n & 1]);
-                            ++n;
-                        } else if (ok) {
-                            mbar_arrive(&sm.v_empty[cv.stage]);
+                                mma_ts(tmem + T::o(x), tmem + T::s(x, b) + 8 * k, vd + (2048 * k >> 4), id_o,
+                                       u > 0 || k > 0 ? 1u : 0u);
+                            mma_commit(&sm.o_full[x][b]);
+                            ++n[x];
                         }
                         cv.next(args.v_stages);
                     }
@@ -677,54 +697,65 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                     if (t.n <= 0) break;
                 }
                 if (!ok) {
-                    mma_commit(&sm.drain[2 + x]);
-                    mbar_wait(&sm.drain[2 + x], 0, kWaitNs);
+                    mma_commit(&sm.drain[1]);
+                    mbar_wait(&sm.drain[1], 0, kWaitNs);
                 }
             }
             __syncwarp();
-        } else if (!k8 && warp == 12) {
-            // ---- feed: 16-bit pages -------------------------------------------------------
+        } else if (warp == 10) {
+            // ---- pages: K of a unit comes a unit before V ----------------------------------------
             const int page_rows = 1 << a.kv.page_shift, box = min(page_rows, kUnit), boxes = kUnit / box;
+            constexpr int kRowBytes = k8 ? 64 : 128;     // of a 64-dim half
             const int p = lane / kHalves, h = lane % kHalves;
             unsigned unit = 0, n_tail = 0;
-            Cursor ck, cv;
+            Cursor ck, cv;                               // 8-bit pages: ck counts the tiles of codes, K and V
             bool ok = true;
-            // Stores K (kv = 0) or V of unit u of the tile; `ordinal` is the unit's number in the CTA.
-            const auto feed = [&](int u, int kv, unsigned ordinal) {
-                Cursor& cur = kv ? cv : ck;
-                uint64_t* full = kv ? &sm.v_full[cur.stage] : &sm.k_full[cur.stage];
-                uint64_t* empty = kv ? &sm.v_empty[cur.stage] : &sm.k_empty[cur.stage];
+            // This lane's page of a unit of the tile, -1 for none (as read: checked when used).
+            const auto look_up = [&](int u) {
+                const int key = (t.u0 + u) * kUnit + p * box;
+                if (u >= t.n || p >= boxes || key >= t.keys) return -1;
+                return __ldg(a.b.pages + (long long)t.s * a.b.pages_stride + (key >> a.kv.page_shift));
+            };
+            // Asks for K (kv = 0) or V of unit u of the tile; `ordinal` is the unit's number in the CTA.
+            const auto feed = [&](int u, int kv, int page, unsigned ordinal) {
+                Cursor& cur = kv && !k8 ? cv : ck;
+                uint64_t* full = k8 ? &sm.raw_full[cur.stage] : kv ? &sm.v_full[cur.stage] : &sm.k_full[cur.stage];
+                uint64_t* empty = k8 ? &sm.raw_empty[cur.stage] : kv ? &sm.v_empty[cur.stage] : &sm.k_empty[cur.stage];
                 const int key0 = (t.u0 + u) * kUnit, key = key0 + p * box;
-                int page = -1;
-                bool is_bad = false;
-                if (p < boxes && key < t.keys) {
-                    page = __ldg(a.b.pages + (long long)t.s * a.b.pages_stride + (key >> a.kv.page_shift));
-                    if ((unsigned)page >= (unsigned)a.kv.n_pages) {
-                        is_bad = true;
-                        page = -1;
-                        raise_guard(a.b.guard, QWEN2_GUARD_PAGE);
-                    }
+                const bool is_bad = p < boxes && key < t.keys && (unsigned)page >= (unsigned)a.kv.n_pages;
+                if (is_bad) {
+                    page = -1;
+                    raise_guard(a.b.guard, QWEN2_GUARD_PAGE);
                 }
                 const unsigned bad =
                     __reduce_or_sync(0xffffffffu, is_bad ? ((1u << (box / 16)) - 1) << (p * box / 16) : 0u);
-                const unsigned bytes = (unsigned)(__popc(__ballot_sync(0xffffffffu, page >= 0)) * box * 128);
-                const bool patch = kv && (key0 + kUnit > t.keys || bad);   // positions that are no keys: zeros in V
+                unsigned bytes = (unsigned)(__popc(__ballot_sync(0xffffffffu, page >= 0)) * box * kRowBytes);
+                if (k8 && !kv) bytes += bytes / (kHalves * kRowBytes) * 8;               // and their scales
+                const bool patch = !k8 && kv && (key0 + kUnit > t.keys || bad);          // positions that are no keys: zeros in V
                 if (cur.round) ok = __all_sync(0xffffffffu, wait(empty, (cur.round - 1) & 1, sm, a.b.guard));
                 if (!ok) return;
+                const int off = key & (page_rows - 1);
                 int at[3];
-                at[args.kv_rank[0]] = key & (page_rows - 1);
+                at[args.kv_rank[0]] = off;
                 at[args.kv_rank[1]] = t.head;
                 at[args.kv_rank[2]] = page;
-                const uint32_t tile = (kv ? v_ring : k_ring) + cur.stage * kTile;
+                const uint32_t tile = k8 ? raw_ring + cur.stage * kRaw : (kv ? v_ring : k_ring) + cur.stage * kTile;
                 uint64_t* bar = patch ? &sm.tail : full;
                 if (lane == 0) {
-                    if (!kv) sm.bad[ordinal % kLag] = bad;
+                    if (!kv) sm.bad[ordinal % kBadLag] = bad;
                     mbar_expect_tx(bar, bytes);
                 }
                 __syncwarp();
-                if (page >= 0)
-                    tma_load_4d(tile + h * kHalfBytes + p * box * 128, kv ? &tm_v : &tm_k, 64 * h, at[0], at[1], at[2], bar);
-                cur.next(kv ? args.v_stages : args.k_stages);
+                if (page >= 0) {
+                    tma_load_4d(tile + (h * kUnit + p * box) * kRowBytes, kv ? &tm_v : &tm_k, 64 * h, at[0], at[1], at[2], bar);
+                    if (k8 && !kv && h == 0) {
+                        const long long i = (((long long)page * a.kv.n_kv + t.head) << a.kv.page_shift) + off;
+                        const uint32_t to = tile + kHalves * kUnit * 64 + 4 * p * box;
+                        bulk_load(to, a.kv.k_scale + i, 4 * box, bar);
+                        bulk_load(to + 4 * kUnit, a.kv.v_scale + i, 4 * box, bar);
+                    }
+                }
+                cur.next(k8 ? args.raw_stages : kv ? args.v_stages : args.k_stages);
                 if (patch) {
                     ok = __all_sync(0xffffffffu, wait(&sm.tail, n_tail & 1, sm, a.b.guard));
                     if (!ok) mbar_wait(&sm.tail, n_tail & 1, kWaitNs);
@@ -744,144 +775,115 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                 }
             };
             while (ok) {
-                feed(0, 0, unit);
+                // Pages are looked up two units ahead of their use.
+                int page0 = look_up(0), page1 = look_up(1), page2 = look_up(2);    // of units u, u + 1, u + 2
+                feed(0, 0, page0, unit);
                 for (int u = 0; u < t.n && ok; ++u) {
-                    if (u + 1 < t.n) feed(u + 1, 0, unit + u + 1);
-                    if (ok) feed(u, 1, unit + u);
+                    const int page3 = look_up(u + 3);
+                    if (u + 1 < t.n) feed(u + 1, 0, page1, unit + u + 1);
+                    if (ok) feed(u, 1, page0, unit + u);
+                    page0 = page1;
+                    page1 = page2;
+                    page2 = page3;
                 }
                 unit += t.n;
                 next_tile<kUnit, kCost>(a, work, t);
                 if (t.n <= 0) break;
             }
             if (!ok) {   // copies in flight land before the shared memory is given back
-                for (int i = 0; i < kMaxStages; ++i) {   // each stage's last entry
-                    if (i < ck.stage || (ck.round && i < args.k_stages))
-                        mbar_wait(&sm.k_full[i], (i < ck.stage ? ck.round : ck.round - 1) & 1, kWaitNs);
-                    if (i < cv.stage || (cv.round && i < args.v_stages))
-                        mbar_wait(&sm.v_full[i], (i < cv.stage ? cv.round : cv.round - 1) & 1, kWaitNs);
+                const auto last = [&](uint64_t* full, const Cursor& c, int stages) {   // each stage's last entry
+                    for (int i = 0; i < stages; ++i)
+                        if (i < c.stage || c.round) mbar_wait(&full[i], (i < c.stage ? c.round : c.round - 1) & 1, kWaitNs);
+                };
+                if (k8) last(sm.raw_full, ck, args.raw_stages);
+                else {
+                    last(sm.k_full, ck, args.k_stages);
+                    last(sm.v_full, cv, args.v_stages);
                 }
             }
             __syncwarp();
         } else if (k8 && warp >= 12) {
-            // ---- feed: 8-bit pages ------------------------------------------------------
-            // Thread e takes 16-byte piece e % 4 of row e / 4 (+ 32) of each 64-dim half:
-            // two adjacent rows' pieces fill all banks.
+            // ---- codes to tiles ---------------------------------------------------------------------
+            // Thread e takes 16-byte piece e % 4 of row e / 4 (+ 32) of each 64-dim half: two adjacent
+            // rows' pieces fill all banks, of the codes and of the tiles.
             const int e0 = tid - 384, piece = e0 & 3, row0 = e0 >> 2;
-            constexpr int kPieces = 2 * kHalves;        // per thread and tile
             unsigned unit = 0;
-            Cursor ck, cv;
+            Cursor cr, ck, cv;
             bool ok = true;
             int g = -100;
-            // The codes of K or V of a unit on their way, and for K the scales of its positions
-            // lane and lane + 32 (every warp has all of them, and so the same G).
-            struct Load {
-                uint4 raw[kPieces];
-                float ks[2], vs[2];
-                unsigned bad;
-            };
-            // Lane l's page of positions 16 (l % 4) .. of a unit: -1 for none (as read: it is
-            // checked when it is used, a turn later).
-            const auto look_up = [&](int u) {
-                const int key = (t.u0 + u) * kUnit + 16 * (lane & 3);
-                if (u >= t.n || key >= t.keys) return -1;
-                return __ldg(a.b.pages + (long long)t.s * a.b.pages_stride + (key >> a.kv.page_shift));
-            };
-            const auto load = [&](int u, int kv, int page_l, Load& ld) {
-                const int key0 = (t.u0 + u) * kUnit, mask = (1 << a.kv.page_shift) - 1;
-                const bool there = key0 + 16 * (lane & 3) < t.keys;
-                if ((unsigned)page_l >= (unsigned)a.kv.n_pages) page_l = -1;
+            const auto store = [&](int u, int kv, unsigned ordinal) {
+                Cursor& cur = kv ? cv : ck;
+                ok = wait(&sm.raw_full[cr.stage], cr.round & 1, sm, a.b.guard);
+                if (cur.round)
+                    ok = ok && wait(kv ? &sm.v_empty[cur.stage] : &sm.k_empty[cur.stage], (cur.round - 1) & 1, sm, a.b.guard);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return;
+                const int key0 = (t.u0 + u) * kUnit;
+                const unsigned bad = sm.bad[ordinal % kBadLag];
+                const uint32_t raw = raw_ring + cr.stage * kRaw;
+                const auto is_key = [&](int r) { return key0 + r < t.keys && !(bad >> (r / 16) & 1); };
                 if (!kv) {
-                    ld.bad = __ballot_sync(0xffffffffu, there && page_l < 0) & 0xfu;
-                    if (ld.bad && lane == 0) raise_guard(a.b.guard, QWEN2_GUARD_PAGE);
-                }
-                const char* base = kv ? a.kv.v : a.kv.k;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int r = row0 + 32 * j, pg = __shfl_sync(0xffffffffu, page_l, r >> 4);
-                    const bool in = pg >= 0 && key0 + r < t.keys;
-                    const char* src = base + (in ? (long long)pg * a.kv.page_bytes +
-                                                       (long long)((key0 + r) & mask) * a.kv.token_bytes +
-                                                       (long long)t.head * a.kv.head_bytes
-                                                 : 0) + 16 * piece;
-#pragma unroll
-                    for (int h = 0; h < kHalves; ++h)
-                        ld.raw[2 * h + j] = in ? ld_stream_v4(src + 64 * h) : make_uint4(0, 0, 0, 0);
-                }
-                if (!kv) {
+                    // Every warp has all the unit's v scales, and so the same G.
+                    float ks[2], vs[2];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int r = lane + 32 * j, pg = __shfl_sync(0xffffffffu, page_l, r >> 4);
-                        ld.ks[j] = ld.vs[j] = 0.f;
-                        if (pg >= 0 && key0 + r < t.keys) {
-                            const long long i = (((long long)pg * a.kv.n_kv + t.head) << a.kv.page_shift) + ((key0 + r) & mask);
-                            ld.ks[j] = __ldg(a.kv.k_scale + i);
-                            ld.vs[j] = __ldg(a.kv.v_scale + i);
-                        }
+                        const int r = lane + 32 * j;
+                        const uint32_t from = raw + kHalves * kUnit * 64 + 4 * r;
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks[j]) : "r"(from) : "memory");
+                        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs[j]) : "r"(from + 4 * kUnit) : "memory");
+                        if (!is_key(r)) ks[j] = vs[j] = 0.f;
                     }
-                }
-            };
-            const auto store = [&](int kv, unsigned ordinal, const Load& ld) {
-                Cursor& cur = kv ? cv : ck;
-                if (cur.round)
-                    ok = __all_sync(0xffffffffu, ok && wait(kv ? &sm.v_empty[cur.stage] : &sm.k_empty[cur.stage],
-                                                            (cur.round - 1) & 1, sm, a.b.guard));
-                if (!ok) return;
-                if (!kv) {
-                    const unsigned slot = ordinal % kLag;
-                    g = max(g, ceil_log2(warp_max(fmaxf(ld.vs[0], ld.vs[1]))));
+                    g = max(g, ceil_log2(warp_max(fmaxf(vs[0], vs[1]))));
                     if (warp == 12) {
+                        const unsigned slot = ordinal % kLag;
                         const float down = pow2i(-g);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const uint32_t at = scales + slot * (2 * kUnit * 4) + 4 * (lane + 32 * j);
-                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(ld.ks[j]) : "memory");
-                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * kUnit), "f"(ld.vs[j] * down) : "memory");
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(ks[j]) : "memory");
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 4 * kUnit), "f"(vs[j] * down) : "memory");
                         }
-                        if (lane == 0) {
-                            sm.g[slot] = g;
-                            sm.bad[slot] = ld.bad;
-                        }
+                        if (lane == 0) sm.g[slot] = g;
                     }
                 }
                 const uint32_t tile = (kv ? v_ring : k_ring) + cur.stage * kTile;
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    uint32_t o[8];
-                    widen16<K, BF16>(ld.raw[i], o);
-                    const int r = row0 + 32 * (i & 1);
-                    const uint32_t at = tile + (i >> 1) * kHalfBytes + r * 128;
+                for (int j = 0; j < 2; ++j) {
+                    const int r = row0 + 32 * j;
+                    const bool in = is_key(r);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         at + (((2 * piece + j) ^ (r & 7)) << 4)),
-                                     "r"(o[4 * j]), "r"(o[4 * j + 1]), "r"(o[4 * j + 2]), "r"(o[4 * j + 3])
+                    for (int c = 0; c < kHalves; ++c) {
+                        uint4 w;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                                     : "r"(raw + (c * kUnit + r) * 64 + 16 * piece)
                                      : "memory");
+                        uint32_t o[8];
+                        widen16<K, BF16>(in ? w : make_uint4(0, 0, 0, 0), o);
+                        const uint32_t at = tile + c * kHalfBytes + r * 128;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             at + (((2 * piece + i) ^ (r & 7)) << 4)),
+                                         "r"(o[4 * i]), "r"(o[4 * i + 1]), "r"(o[4 * i + 2]), "r"(o[4 * i + 3])
+                                         : "memory");
+                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(kv ? &sm.v_full[cur.stage] : &sm.k_full[cur.stage]);
+                if (lane == 0) {
+                    mbar_arrive(kv ? &sm.v_full[cur.stage] : &sm.k_full[cur.stage]);
+                    mbar_arrive(&sm.raw_empty[cr.stage]);
+                }
+                cr.next(args.raw_stages);
                 cur.next(kv ? args.v_stages : args.k_stages);
             };
             while (ok) {
                 g = -100;
-                // K of a unit is stored a unit before V.  The codes stored in a turn were asked for
-                // in the turn before, their pages in the one before that.
-                Load k[2], v[2];
-                int page0 = look_up(0), page1 = look_up(1), page2;    // of units u, u + 1, u + 2 below
-                load(0, 0, page0, k[0]);
-                if (t.n > 1) load(1, 0, page1, k[1]);
-                load(0, 1, page0, v[0]);
-                page2 = look_up(2);
-                store(0, unit, k[0]);
-#pragma unroll 2
+                store(0, 0, unit);
                 for (int u = 0; u < t.n && ok; ++u) {
-                    const int page3 = look_up(u + 3);
-                    if (u + 2 < t.n) load(u + 2, 0, page2, k[u & 1]);
-                    if (u + 1 < t.n) load(u + 1, 1, page1, v[(u + 1) & 1]);
-                    if (u + 1 < t.n) store(0, unit + u + 1, k[(u + 1) & 1]);
-                    if (ok) store(1, unit + u, v[u & 1]);
-                    page1 = page2;
-                    page2 = page3;
+                    if (u + 1 < t.n) store(u + 1, 0, unit + u + 1);
+                    if (ok) store(u, 1, unit + u);
                 }
                 unit += t.n;
                 next_tile<kUnit, kCost>(a, work, t);
@@ -901,16 +903,17 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
 // A pool's tensor map: 64 dims of `box` positions of one head and page per
 // copy.  The dims stand in the order of their strides, rank[] says where
 // position, head and page went.
-bool encode_pool(CUtensorMap* m, const char* base, const Pool& kv, int head_dim, bool bf16, int (&rank)[3]) {
+bool encode_pool(CUtensorMap* m, const char* base, const Pool& kv, int head_dim, int format, int (&rank)[3]) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const int page = 1 << kv.page_shift;
+    const bool k8 = format == QWEN2_KV_INT8 || format == QWEN2_KV_E4M3;
     long long stride[3] = {kv.token_bytes, kv.head_bytes, kv.page_bytes};
     const unsigned long long size[3] = {(unsigned long long)page, (unsigned long long)kv.n_kv,
                                         (unsigned long long)kv.n_pages};
     // A dim of one element may have any stride.
     for (int i = 0; i < 3; ++i)
-        if (size[i] == 1) stride[i] = (long long)head_dim * 2 << 20;
+        if (size[i] == 1) stride[i] = (long long)head_dim << 20;
     int order[3] = {0, 1, 2};
     for (int i = 0; i < 2; ++i)
         for (int j = 0; j < 2 - i; ++j)
@@ -929,9 +932,10 @@ bool encode_pool(CUtensorMap* m, const char* base, const Pool& kv, int head_dim,
         strides[i] = (cuuint64_t)stride[d];
         if (d == 0) box[1 + i] = (cuuint32_t)(page < kUnit ? page : kUnit);
     }
-    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+    return enc(m, k8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                     : format == QWEN2_KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                const_cast<char*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               k8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -955,11 +959,20 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap
     auto kern = k_paged_attn_tc<HD, BF16, K>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
-    const int rest = kStaging + 8 * (args.a.b.n_seq + 1) + (K == kSame16 ? 0 : kLag * 2 * kUnit * 4);
-    const int tiles = (227 * 1024 - 1024 - kHead - rest - 2 * kQTile) / kTile;
-    args.k_stages = min(kMaxStages, tiles / 2);
-    args.v_stages = min(kMaxStages, tiles - args.k_stages);
-    const size_t smem = 1024 + kHead + 2 * kQTile + (size_t)(args.k_stages + args.v_stages) * kTile + rest;
+    constexpr int kRaw = HD * kUnit + kRawScales;
+    int rest = kStaging + 8 * (args.a.b.n_seq + 1) + 2 * kQTile;
+    const int room = 227 * 1024 - 1024 - kHead;
+    if constexpr (K == kSame16) {
+        const int tiles = (room - rest) / kTile;
+        args.k_stages = min(kMaxStages, tiles / 2);
+        args.v_stages = min(kMaxStages, tiles - args.k_stages);
+    } else {
+        // 4,096 sequences leave room for two K and V tiles at head_dim 128.
+        rest += kLag * 2 * kUnit * 4;
+        args.k_stages = args.v_stages = room - rest >= 2 * kTiles8 * kTile + 4 * kRaw ? kTiles8 : 2;
+        args.raw_stages = min(kMaxRaw, (room - rest - 2 * args.k_stages * kTile) / kRaw);
+    }
+    const size_t smem = 1024 + kHead + (size_t)(args.k_stages + args.v_stages) * kTile + args.raw_stages * kRaw + rest;
     if (chained) return launch_pdl(kern, dim3(n_sm), dim3(kThreads), smem, st, q, k, v, args);
     kern<<<n_sm, kThreads, smem, st>>>(q, k, v, args);
     return cudaGetLastError();
@@ -983,12 +996,8 @@ bool tc_encode(TcMaps& m, const Pool& kv, const AttnCall& c, const Rows& q, int 
     const int group = c.n_head / kv.n_kv;
     int rank_v[3];
     if (!encode_q(&m.q, q, n_rows, c.n_head, group, 128 / group, c.head_dim, bf16)) return false;
-    if (c.format == QWEN2_KV_INT8 || c.format == QWEN2_KV_E4M3) {
-        m.k = m.v = m.q;      // not used
-        return true;
-    }
-    return encode_pool(&m.k, kv.k, kv, c.head_dim, bf16, m.kv_rank) &&
-           encode_pool(&m.v, kv.v, kv, c.head_dim, bf16, rank_v);
+    return encode_pool(&m.k, kv.k, kv, c.head_dim, c.format, m.kv_rank) &&
+           encode_pool(&m.v, kv.v, kv, c.head_dim, c.format, rank_v);
 }
 
 cudaError_t enqueue_attention_tc(const TcMaps& m, const AttnArgs& a, int format, int head_dim, bool bf16, int n_sm,
