@@ -105,13 +105,28 @@ struct TcArgs {
     int min_slots;
 };
 
+// The roles' loops together have to stay within the instruction cache (inlined
+// everywhere, the slow part of the waits and the walk over the work list made
+// instruction fetches the largest stall of the 8-bit kernels): those are calls.
+__device__ __noinline__ WorkList tc_build_work(const AttnArgs& a, long long* prefix, int min_slots) {
+    return build_work<kUnit, kCost>(a, prefix, min_slots);
+}
+__device__ __noinline__ Tile tc_find_tile(const AttnArgs& a, const WorkList& w) { return find_tile<kUnit, kCost>(a, w); }
+__device__ __noinline__ void tc_next_tile(const AttnArgs& a, const WorkList& w, Tile& t) {
+    next_tile<kUnit, kCost>(a, w, t);
+}
+__device__ __noinline__ void tc_note_open(const AttnArgs& a, const WorkList& w, const Tile& t) {
+    note_open<kCost>(a, w, t);
+}
+
 // Waits for the phase of parity `parity`, at most about kWaitNs: the SM's own
 // clock is read (a read of the global timer costs a large part of a unit's
 // time).  False once this or another wait of the block has given up.
 constexpr long long kWaitClocks = (long long)kWaitNs * 2;      // 2 s or more at up to 2 GHz
-__device__ __forceinline__ bool wait_slow(uint64_t* bar, unsigned parity, TcSmem& sm, int* guard) {
+__device__ __noinline__ bool wait_slow(uint64_t* bar, unsigned parity, TcSmem& sm, int* guard) {
     const long long t0 = clock64();
     for (;;) {
+#pragma unroll 1
         for (int i = 0; i < 32; ++i)
             if (mbar_try_wait(bar, parity)) return true;
         if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
@@ -212,6 +227,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // A place in the ring of K tiles or of V tiles: stored and used in order.
@@ -309,6 +332,17 @@ __device__ __forceinline__ void put_rows64(uint32_t stage, const uint32_t (&w)[1
     }
 }
 
+// The i-th of the 2 n tiles of n units in the order they are loaded, K of a
+// unit before V of the one before it (K0 K1 V0 K2 V1 ... V of the last): 0 for
+// K, 1 for V of unit u.  The loops over it have one copy of their body: the
+// warps' roles together have to stay within the instruction cache (three
+// copies of the widening loop made fetches the largest stall by far).
+__device__ __forceinline__ int in_order(int i, int n, int& u) {
+    const bool last = i == 2 * n - 1, v = last || (i > 0 && !(i & 1));
+    u = last ? n - 1 : v ? i / 2 - 1 : (i + 1) / 2;
+    return v;
+}
+
 // 16 codes as 16-bit values, in order; exact.
 template <Kind K, bool BF16>
 __device__ __forceinline__ void widen16(const uint4& raw, uint32_t (&o)[8]) {
@@ -374,12 +408,14 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
 
     pdl_launch_dependents();
     if (tid == 0) {
+#pragma unroll 1
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sm.k_full[i], k8 ? kFeeders : 1);
             mbar_init(&sm.v_full[i], k8 ? kFeeders : 1);
             mbar_init(&sm.k_empty[i], 2);
             mbar_init(&sm.v_empty[i], 2);
         }
+#pragma unroll 1
         for (int i = 0; i < kMaxRaw; ++i) {
             mbar_init(&sm.raw_full[i], 1);
             mbar_init(&sm.raw_empty[i], kFeeders);
@@ -405,14 +441,14 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    const WorkList work = build_work<kUnit, kCost>(a, prefix, args.min_slots);
+    const WorkList work = tc_build_work(a, prefix, args.min_slots);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_slot;
     bool open = false;
     if (work.begin < work.end) {
-        Tile t = find_tile<kUnit, kCost>(a, work);
+        Tile t = tc_find_tile(a, work);
         if (warp < 8) {
             // ---- softmax of half x --------------------------------------------------
             const int x = warp >> 2, rl = 32 * (warp & 3) + lane;
@@ -423,6 +459,7 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
             unsigned unit = 0;         // units of the CTA before this tile
             Cursor ck, cv;             // K of the current unit; V of the oldest unit not yet released
             bool ok = true;
+#pragma unroll 1
             while (ok) {
                 const int packed0 = t.t * a.tile, packed = t.q.n * a.group;
                 const int i = packed0 + x * args.sub + rl;
@@ -432,6 +469,7 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                     const int sure = min(row_limit(a, t.q, packed0 + x * args.sub), t.keys - 1);
                     float m = -INFINITY, l0 = 0.f, l1 = 0.f;
                     int g = -100;          // log2 of G
+#pragma unroll 1
                     for (int u = 0; u < t.n; ++u, ++n_s) {
                         const int key0 = (t.u0 + u) * kUnit;
                         const uint32_t t_s = lanes + T::s(x, n_s & 1);
@@ -462,20 +500,17 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                             scale_scores(s[1], at + 128);
                         }
                         if (key0 + kUnit - 1 > sure || bad) {
-                            const int last = lim - key0;      // last position of the unit the row sees
+                            // A bit for each position that the row sees.
+                            const int last = lim - key0;
+                            unsigned long long see = last >= kUnit - 1 ? ~0ull : last < 0 ? 0ull : (2ull << last) - 1;
 #pragma unroll
-                            for (int c = 0; c < 2; ++c)
-                                if (__any_sync(0xffffffffu, last < 32 * c + 31)) {
+                            for (int c = 0; c < 4; ++c)
+                                if (bad >> c & 1) see &= ~(0xffffull << (16 * c));
+                            const uint32_t lo = (uint32_t)see, hi = (uint32_t)(see >> 32);
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e)
-                                        if (32 * c + e > last) s[c][e] = 0xff800000u;
-                                }
-                            if (bad) {
-#pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    if (bad >> c & 1)
-#pragma unroll
-                                        for (int e = 0; e < 16; ++e) s[c / 2][16 * (c % 2) + e] = 0xff800000u;
+                            for (int e = 0; e < 32; ++e) {
+                                if (!(lo >> e & 1)) s[0][e] = 0xff800000u;
+                                if (!(hi >> e & 1)) s[1][e] = 0xff800000u;
                             }
                         }
                         float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -519,22 +554,25 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                             }
                         }
                         const float base = m == -INFINITY ? 0.f : -m;
-                        uint32_t p[32];
-                        [[maybe_unused]] float4 vs;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float y = __uint_as_float(s[e / 16][2 * e % 32]), z = __uint_as_float(s[e / 16][2 * e % 32 + 1]);
-                            fma2(y, z, sc, base);
-                            y = ex2(y);
-                            z = ex2(z);
-                            add2(l0, l1, y, z);
-                            if constexpr (k8) {
-                                if (e % 2 == 0) vs = lds4(at + 4 * kUnit + 8 * e);
-                                mul2(y, z, e % 2 ? vs.z : vs.x, e % 2 ? vs.w : vs.y);
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t p[16];
+                            [[maybe_unused]] float4 vs;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float y = __uint_as_float(s[c][2 * e]), z = __uint_as_float(s[c][2 * e + 1]);
+                                fma2(y, z, sc, base);
+                                y = ex2(y);
+                                z = ex2(z);
+                                add2(l0, l1, y, z);
+                                if constexpr (k8) {
+                                    if (e % 2 == 0) vs = lds4(at + 4 * kUnit + 128 * c + 8 * e);
+                                    mul2(y, z, e % 2 ? vs.z : vs.x, e % 2 ? vs.w : vs.y);
+                                }
+                                p[e] = pack2<BF16>(y, z);
                             }
-                            p[e] = pack2<BF16>(y, z);
+                            tmem_st16(t_s + 16 * c, p);
                         }
-                        tmem_st32(t_s, p);
                         tmem_st_wait();
                         tc_fence_before();
                         mbar_arrive(&sm.p_full[x][n_s & 1]);
@@ -546,6 +584,7 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                     ok = __all_sync(0xffffffffu, ok && wait(&sm.o_full[x][(n_s - 1) & 1], (n_s - 1) >> 1 & 1, sm, a.b.guard));
                     if (!ok) break;
                     tc_fence_after();
+#pragma unroll 1
                     for (int u = max(0, t.n - 2); u < t.n; ++u) {
                         if (rl == 0) mbar_arrive(&sm.v_empty[cv.stage]);
                         cv.next(args.v_stages);
@@ -595,17 +634,18 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                     }
                     if (!place.whole && place.begins) {
                         open = true;
-                        if (tid == 0) note_open<kCost>(a, work, t);
+                        if (tid == 0) tc_note_open(a, work, t);
                     }
                     tc_fence_before();
                 } else {
+#pragma unroll 1
                     for (int u = 0; u < t.n; ++u) {
                         ck.next(args.k_stages);
                         cv.next(args.v_stages);
                     }
                 }
                 unit += t.n;
-                next_tile<kUnit, kCost>(a, work, t);
+                tc_next_tile(a, work, t);
                 if (t.n <= 0) break;
             }
         } else if (warp == 8) {
@@ -615,6 +655,7 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                 unsigned n[2] = {0, 0}, seg = 0;       // units of each half, tiles
                 Cursor ck;
                 bool ok = true;
+#pragma unroll 1
                 for (;; ++seg) {
                     const int halves = t.t * a.tile + args.sub < t.q.n * a.group ? 2 : 1;
                     if (seg) ok = wait(&sm.q_empty, (seg - 1) & 1, sm, a.b.guard);
@@ -625,6 +666,7 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                             tma_load_3d(q_tiles + x * kQTile + c * kQBytes, &tm_q, 64 * c, t.head * a.group,
                                         t.q.q0 + (2 * t.t + x) * args.sub_rows, &sm.q_full);
                     ok = wait(&sm.q_full, seg & 1, sm, a.b.guard);
+#pragma unroll 1
                     for (int u = 0; u < t.n && ok; ++u) {
                         ok = wait(&sm.k_full[ck.stage], ck.round & 1, sm, a.b.guard);
                         const uint64_t kd = desc_sw128(k_ring + ck.stage * kTile);
@@ -652,7 +694,7 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                         ck.next(args.k_stages);
                     }
                     if (ok && halves == 1) mbar_arrive(&sm.q_empty);
-                    next_tile<kUnit, kCost>(a, work, t);
+                    tc_next_tile(a, work, t);
                     if (t.n <= 0 || !ok) break;
                 }
                 if (!ok) {   // what is in flight ends before the memory is given back
@@ -669,8 +711,10 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                 unsigned n[2] = {0, 0};
                 Cursor cv;
                 bool ok = true;
+#pragma unroll 1
                 while (ok) {
                     const int halves = t.t * a.tile + args.sub < t.q.n * a.group ? 2 : 1;
+#pragma unroll 1
                     for (int u = 0; u < t.n && ok; ++u) {
                         ok = wait(&sm.v_full[cv.stage], cv.round & 1, sm, a.b.guard);
                         const uint64_t vd = desc_mn128(v_ring + cv.stage * kTile);
@@ -693,7 +737,7 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                         }
                         cv.next(args.v_stages);
                     }
-                    next_tile<kUnit, kCost>(a, work, t);
+                    tc_next_tile(a, work, t);
                     if (t.n <= 0) break;
                 }
                 if (!ok) {
@@ -761,6 +805,7 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                     if (!ok) mbar_wait(&sm.tail, n_tail & 1, kWaitNs);
                     ++n_tail;
                     // Eight lanes a 128-byte row, four rows a store.
+#pragma unroll 1
                     for (int r = (bad ? 0 : max(0, t.keys - key0) & ~3) + (lane >> 3); r < kUnit; r += 4)
                         if (key0 + r >= t.keys || (bad >> (r / 16) & 1))
 #pragma unroll
@@ -774,24 +819,34 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                     if (lane == 0) mbar_arrive(full);
                 }
             };
+#pragma unroll 1
             while (ok) {
-                // Pages are looked up two units ahead of their use.
-                int page0 = look_up(0), page1 = look_up(1), page2 = look_up(2);    // of units u, u + 1, u + 2
-                feed(0, 0, page0, unit);
-                for (int u = 0; u < t.n && ok; ++u) {
-                    const int page3 = look_up(u + 3);
-                    if (u + 1 < t.n) feed(u + 1, 0, page1, unit + u + 1);
-                    if (ok) feed(u, 1, page0, unit + u);
-                    page0 = page1;
-                    page1 = page2;
-                    page2 = page3;
+                // One copy of the code for K and V (see in_order): pages are looked up two units
+                // ahead of K, and kept until V.
+                int k0 = look_up(0), k1 = look_up(1), v0 = -1, v1 = -1, held = 0;
+#pragma unroll 1
+                for (int i = 0; i < 2 * t.n && ok; ++i) {
+                    int u;
+                    const int kv = in_order(i, t.n, u);
+                    const int page = kv ? v0 : k0;
+                    if (kv) {
+                        v0 = v1;
+                        --held;
+                    } else {
+                        if (held++) v1 = k0;
+                        else v0 = k0;
+                        k0 = k1;
+                        k1 = look_up(u + 2);
+                    }
+                    feed(u, kv, page, unit + u);
                 }
                 unit += t.n;
-                next_tile<kUnit, kCost>(a, work, t);
+                tc_next_tile(a, work, t);
                 if (t.n <= 0) break;
             }
             if (!ok) {   // copies in flight land before the shared memory is given back
                 const auto last = [&](uint64_t* full, const Cursor& c, int stages) {   // each stage's last entry
+#pragma unroll 1
                     for (int i = 0; i < stages; ++i)
                         if (i < c.stage || c.round) mbar_wait(&full[i], (i < c.stage ? c.round : c.round - 1) & 1, kWaitNs);
                 };
@@ -878,15 +933,17 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                 cr.next(args.raw_stages);
                 cur.next(kv ? args.v_stages : args.k_stages);
             };
+#pragma unroll 1
             while (ok) {
                 g = -100;
-                store(0, 0, unit);
-                for (int u = 0; u < t.n && ok; ++u) {
-                    if (u + 1 < t.n) store(u + 1, 0, unit + u + 1);
-                    if (ok) store(u, 1, unit + u);
+#pragma unroll 1
+                for (int i = 0; i < 2 * t.n && ok; ++i) {
+                    int u;
+                    const int kv = in_order(i, t.n, u);
+                    store(u, kv, unit + u);
                 }
                 unit += t.n;
-                next_tile<kUnit, kCost>(a, work, t);
+                tc_next_tile(a, work, t);
                 if (t.n <= 0) break;
             }
         }
