@@ -386,10 +386,10 @@ int qwen2_quantize_q4_0(const uint16_t *w, int64_t rows, int64_t k, uint8_t *pac
 #define QWEN2_KV_BF16     1   /* bfloat16 */
 #define QWEN2_KV_INT8     2   /* int8 codes in [-127, 127], one f32 scale per (position, kv head):
                                  scale = max|x| / 127 (1 where max|x| = 0),
-                                 code = round-half-away(x / scale); value = scale * code */
+                                 code = round-half-away(x * (1 / scale)); value = scale * code */
 #define QWEN2_KV_E4M3     3   /* 8-bit floats (4 exponent, 3 mantissa bits), one f32 scale per
                                  (position, kv head): scale = max|x| / 448 (1 where max|x| = 0),
-                                 code = e4m3(x / scale), nearest even */
+                                 code = e4m3(x * (1 / scale)), nearest even */
 
 /* Guard codes the paged operators write (first one wins). */
 #define QWEN2_GUARD_POSITION 1  /* a position outside the sequence's pages, the rotation table, or below 0 */

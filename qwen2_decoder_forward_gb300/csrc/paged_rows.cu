@@ -25,24 +25,34 @@ namespace {
 
 constexpr int kRowThreads = 256;
 
-// Eight elements of a row as f32.
+// Eight elements of a row, as they lie in memory and as f32.
 template <int DT>
-__device__ __forceinline__ void load8(const char* p, float (&x)[8]) {
-    if constexpr (DT == QWEN2_DTYPE_F32) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Raw8 {
+    uint4 w[DT == QWEN2_DTYPE_F32 ? 2 : 1];
+};
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load8(const char* p) {
+    Raw8<DT> r;
+    r.w[0] = ld_stream_v4(p);
+    if constexpr (DT == QWEN2_DTYPE_F32) r.w[1] = ld_stream_v4(p + 16);
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ void to_f32(const Raw8<DT>& r, float (&x)[8]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float2 f;
-            if constexpr (DT == QWEN2_DTYPE_F16) f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
+    for (int i = 0; i < (DT == QWEN2_DTYPE_F32 ? 2 : 1); ++i) {
+        const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (DT == QWEN2_DTYPE_F32) {
+                x[4 * i + j] = __uint_as_float(w[j]);
+            } else {
+                float2 f;
+                if constexpr (DT == QWEN2_DTYPE_F16) f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+                else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]));
+                x[2 * j] = f.x;
+                x[2 * j + 1] = f.y;
+            }
         }
     }
 }
@@ -74,15 +84,16 @@ __device__ __forceinline__ uint32_t int8_code(float y) {
     return (uint32_t)(uint8_t)(int8_t)fminf(fmaxf(roundf(y), -127.f), 127.f);
 }
 
-// Eight 8-bit codes of x / scale.
+// Eight 8-bit codes of x / scale, the quotient taken as x times 1 / scale (a
+// division an element was a third of the kernel's instructions).
 template <int FMT>
-__device__ __forceinline__ uint2 pack8_8(const float (&x)[8], float scale) {
+__device__ __forceinline__ uint2 pack8_8(const float (&x)[8], float inv) {
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         float y[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = __fdiv_rn(x[4 * i + j], scale);
+        for (int j = 0; j < 4; ++j) y[j] = x[4 * i + j] * inv;
         if constexpr (FMT == QWEN2_KV_INT8) {
             w[i] = int8_code(y[0]) | int8_code(y[1]) << 8 | int8_code(y[2]) << 16 | int8_code(y[3]) << 24;
         } else {
@@ -124,6 +135,11 @@ struct WriteArgs {
     int n_head;         // 0: no queries
     int slices;         // warps one row's heads are spread over
     int out_bf16;
+};
+
+template <int N>
+struct Int {
+    static constexpr int value = N;
 };
 
 // One warp per (row, slice of its heads): a row's lookups and rotation factors
@@ -197,73 +213,97 @@ __global__ void __launch_bounds__(kRowThreads) k_paged_write(const __grid_consta
             partner = hi ? lane - half : lane + half;
         }
     }
-    const int n_slots = a.n_head + 2 * a.kv.n_kv;
-    // Steps of kHeads heads; every lane of the warp takes every step.
-    for (int h0 = slice * kHeads; h0 < n_slots; h0 += a.slices * kHeads) {
-        const int slot = h0 + sub;
-        const bool live = slot < n_slots;
-        const int kind = slot < a.n_head ? 0 : slot < a.n_head + a.kv.n_kv ? 1 : 2;   // q, k, v
-        const int h = kind == 0 ? slot : kind == 1 ? slot - a.n_head : slot - a.n_head - a.kv.n_kv;
-        const Rows& src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-        float x[8];
+    const long long kv_row = (long long)page * a.kv.page_bytes + (long long)off * a.kv.token_bytes;
+    // Heads [h0, h1) of the queries (kKind 0), keys (1) or values (2); every lane
+    // of the warp takes every step of kHeads heads, kBatch steps' loads in flight.
+    const auto heads = [&](auto kind, int h0, int h1) {
+        constexpr int kKind = decltype(kind)::value;
+        constexpr int kBatch = kKind == 0 ? 4 : 2;
+        const Rows& src = kKind == 0 ? a.q : kKind == 1 ? a.k : a.v;
+        const char* from = src.data + (long long)row * src.row_bytes + 8 * kIn * c;
+        const float* nw = kKind == 0 ? a.q_norm : kKind == 1 ? a.k_norm : nullptr;
+        float w[8];
+        if (kKind != 2 && nw) {
+            const float4 w0 = __ldg(reinterpret_cast<const float4*>(nw + 8 * c));
+            const float4 w1 = __ldg(reinterpret_cast<const float4*>(nw + 8 * c) + 1);
+            w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
+            w[4] = w1.x; w[5] = w1.y; w[6] = w1.z; w[7] = w1.w;
+        }
+        for (; h0 < h1; h0 += kBatch * kHeads) {
+            Raw8<DT> raw[kBatch];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        if (live) load8<DT>(src.data + (long long)row * src.row_bytes + (long long)h * src.head_bytes + 8 * kIn * c, x);
-        const float* nw = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
-        if (a.q_norm || a.k_norm) {
-            float ss = 0.f;
+            for (int b = 0; b < kBatch; ++b) {
+                const int h = h0 + b * kHeads + sub;
+                raw[b] = Raw8<DT>{};
+                if (h < h1) raw[b] = load8<DT>(from + (long long)h * src.head_bytes);
+            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+            for (int b = 0; b < kBatch; ++b) {
+                if (h0 + b * kHeads >= h1) break;
+                const int h = h0 + b * kHeads + sub;
+                float x[8];
+                to_f32<DT>(raw[b], x);
+                if (kKind != 2 && nw) {
+                    float ss = 0.f;
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (nw) {
-                const float r = rms_scale(ss, HD, a.eps);
-                const float4 w0 = __ldg(reinterpret_cast<const float4*>(nw + 8 * c));
-                const float4 w1 = __ldg(reinterpret_cast<const float4*>(nw + 8 * c) + 1);
-                const float wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = x[e] * r * wv[e];
+                    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    const float r = rsqrtf(ss * (1.f / HD) + a.eps);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
+                }
+                if (kKind != 2 && a.rotary) {
+                    float p[8];
+                    if (a.interleaved) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, x[e], partner);
+                    }
+                    if (turns) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], cs[e], __fmul_rn(p[e], sn[e]));
+                    }
+                }
+                if constexpr (kKind == 0) {
+                    if (h < h1)
+                        *reinterpret_cast<uint4*>(a.q_out.data + (long long)row * a.q_out.row_bytes +
+                                                  (long long)h * a.q_out.head_bytes + 16 * c) = pack8_16(x, a.out_bf16);
+                } else {
+                    char* dst = (kKind == 1 ? a.kv.k : a.kv.v) + kv_row + (long long)h * a.kv.head_bytes;
+                    if constexpr (FMT == QWEN2_KV_F16 || FMT == QWEN2_KV_BF16) {
+                        if (h < h1) *reinterpret_cast<uint4*>(dst + 16 * c) = pack8_16(x, FMT == QWEN2_KV_BF16);
+                    } else {
+                        float m = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(x[e]));
+#pragma unroll
+                        for (int o = kLanes / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        const float scale = m == 0.f ? 1.f : __fdiv_rn(m, FMT == QWEN2_KV_INT8 ? 127.f : 448.f);
+                        if (h < h1) {
+                            *reinterpret_cast<uint2*>(dst + 8 * c) = pack8_8<FMT>(x, __fdiv_rn(1.f, scale));
+                            if (c == 0)
+                                (kKind == 1 ? a.kv.k_scale
+                                            : a.kv.v_scale)[(((long long)page * a.kv.n_kv + h) << a.kv.page_shift) + off] = scale;
+                        }
+                    }
+                }
             }
         }
-        if (a.rotary) {
-            float p[8];
-            if (a.interleaved) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, x[e], partner);
-            }
-            if (turns && kind != 2) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], cs[e], __fmul_rn(p[e], sn[e]));
-            }
-        }
-        float scale = 1.f;
-        if constexpr (FMT == QWEN2_KV_INT8 || FMT == QWEN2_KV_E4M3) {
-            float m = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(x[e]));
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-            scale = m == 0.f ? 1.f : __fdiv_rn(m, FMT == QWEN2_KV_INT8 ? 127.f : 448.f);
-        }
-        if (!live) continue;
-        if (kind == 0) {
-            *reinterpret_cast<uint4*>(a.q_out.data + (long long)row * a.q_out.row_bytes +
-                                      (long long)h * a.q_out.head_bytes + 16 * c) = pack8_16(x, a.out_bf16);
-            continue;
-        }
-        char* dst = (kind == 1 ? a.kv.k : a.kv.v) + (long long)page * a.kv.page_bytes +
-                    (long long)off * a.kv.token_bytes + (long long)h * a.kv.head_bytes;
-        if constexpr (FMT == QWEN2_KV_F16 || FMT == QWEN2_KV_BF16) {
-            *reinterpret_cast<uint4*>(dst + 16 * c) = pack8_16(x, FMT == QWEN2_KV_BF16);
-        } else {
-            *reinterpret_cast<uint2*>(dst + 8 * c) = pack8_8<FMT>(x, scale);
-            if (c == 0)
-                (kind == 1 ? a.kv.k_scale : a.kv.v_scale)[(((long long)page * a.kv.n_kv + h) << a.kv.page_shift) + off] =
-                    scale;
-        }
+    };
+    // One warp per row: all its heads.  Otherwise its share of the steps.
+    const int sq = (a.n_head + kHeads - 1) / kHeads, sk = (a.kv.n_kv + kHeads - 1) / kHeads;
+    const bool whole = a.slices == 1;
+    for (int i = slice; i < (whole ? 3 : sq + 2 * sk); i += a.slices) {
+        const int kind = whole ? i : i < sq ? 0 : i < sq + sk ? 1 : 2;
+        const int n = kind == 0 ? a.n_head : a.kv.n_kv;
+        const int h0 = whole ? 0 : kHeads * (kind == 0 ? i : kind == 1 ? i - sq : i - sq - sk);
+        const int h1 = whole ? n : min(n, h0 + kHeads);
+        if (kind == 0) heads(Int<0>{}, h0, h1);
+        else if (kind == 1) heads(Int<1>{}, h0, h1);
+        else heads(Int<2>{}, h0, h1);
     }
 }
 
@@ -438,14 +478,13 @@ cudaError_t enqueue_write(const Pool& kv, const Batch& b, const qwen2_paged_writ
         a.rotary = o->rope ? o->rotary_dim : 0;
         a.interleaved = o->interleaved;
     }
-    // One warp per step of heads while that leaves the device unfilled, so
-    // that a decode step's few rows are one round of loads; one warp per row
-    // once the rows alone fill it, so that a row's lookups are made once.
+    // One warp per row once the rows alone fill the device, so that a row's
+    // lookups are made once; with fewer rows its heads are spread over as many
+    // warps as do, down to one step of heads each (a decode step's few rows are
+    // then one round of loads).
     const int heads = head_dim == 64 ? 4 : 2;
-    const int steps = (n_head + 2 * kv.n_kv + heads - 1) / heads;
-    int per_warp = 1;
-    while (per_warp < steps && (long long)b.n_rows * steps / per_warp > 152 * 32) per_warp *= 2;
-    a.slices = (steps + per_warp - 1) / per_warp;
+    const int steps = (n_head + heads - 1) / heads + 2 * ((kv.n_kv + heads - 1) / heads);
+    a.slices = b.n_rows >= 152 * 8 ? 1 : min(steps, (152 * 24 + b.n_rows - 1) / b.n_rows);
     switch (dtype) {
         case QWEN2_DTYPE_F32: return launch_write_fmt<QWEN2_DTYPE_F32>(a, format, head_dim, st);
         case QWEN2_DTYPE_F16: return launch_write_fmt<QWEN2_DTYPE_F16>(a, format, head_dim, st);
