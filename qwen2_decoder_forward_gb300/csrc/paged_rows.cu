@@ -11,8 +11,10 @@
 // Both are bound by HBM traffic (a dozen flops an element): every element is
 // read once and written once, in 16-byte pieces.  A head of hd dims is the
 // work of hd / 8 lanes, 8 dims each (k_paged_read: 16 codes each for 8-bit
-// pages), so the norm's sum, the largest magnitude and the rotation's
-// partner dims are a few shuffles inside one warp.
+// pages), so the norm's sum and the largest magnitude are a few shuffles
+// inside one warp.  A lane of k_paged_write holds both dims of each pair that
+// the rotation turns: four from each half (or four neighbours and the next
+// four), so the rotation needs none.
 #include <cuda_fp8.h>
 
 #include "paged.cuh"
@@ -23,36 +25,39 @@ namespace paged {
 
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 
-// Eight elements of a row, as they lie in memory and as f32.
+// Four elements of a row, as they lie in memory and as f32.
 template <int DT>
-struct Raw8 {
-    uint4 w[DT == QWEN2_DTYPE_F32 ? 2 : 1];
+struct Raw4 {
+    uint32_t w[DT == QWEN2_DTYPE_F32 ? 4 : 2];
 };
 template <int DT>
-__device__ __forceinline__ Raw8<DT> load8(const char* p) {
-    Raw8<DT> r;
-    r.w[0] = ld_stream_v4(p);
-    if constexpr (DT == QWEN2_DTYPE_F32) r.w[1] = ld_stream_v4(p + 16);
+__device__ __forceinline__ Raw4<DT> load4(const char* p) {
+    Raw4<DT> r;
+    if constexpr (DT == QWEN2_DTYPE_F32) {
+        const uint4 v = ld_stream_v4(p);
+        r.w[0] = v.x;
+        r.w[1] = v.y;
+        r.w[2] = v.z;
+        r.w[3] = v.w;
+    } else {
+        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "l"(p));
+    }
     return r;
 }
 template <int DT>
-__device__ __forceinline__ void to_f32(const Raw8<DT>& r, float (&x)[8]) {
+__device__ __forceinline__ void to_f32(const Raw4<DT>& r, float* x) {
 #pragma unroll
-    for (int i = 0; i < (DT == QWEN2_DTYPE_F32 ? 2 : 1); ++i) {
-        const uint32_t w[4] = {r.w[i].x, r.w[i].y, r.w[i].z, r.w[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if constexpr (DT == QWEN2_DTYPE_F32) {
-                x[4 * i + j] = __uint_as_float(w[j]);
-            } else {
-                float2 f;
-                if constexpr (DT == QWEN2_DTYPE_F16) f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-                else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]));
-                x[2 * j] = f.x;
-                x[2 * j + 1] = f.y;
-            }
+    for (int j = 0; j < (DT == QWEN2_DTYPE_F32 ? 4 : 2); ++j) {
+        if constexpr (DT == QWEN2_DTYPE_F32) {
+            x[j] = __uint_as_float(r.w[j]);
+        } else {
+            float2 f;
+            if constexpr (DT == QWEN2_DTYPE_F16) f = __half22float2(*reinterpret_cast<const __half2*>(&r.w[j]));
+            else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.w[j]));
+            x[2 * j] = f.x;
+            x[2 * j + 1] = f.y;
         }
     }
 }
@@ -71,6 +76,10 @@ __device__ __forceinline__ uint4 pack8_16(const float (&x)[8], bool bf16) {
                       pack2(x[6], x[7], bf16));
 }
 
+__device__ __forceinline__ uint2 pack4_16(const float* x, bool bf16) {
+    return make_uint2(pack2(x[0], x[1], bf16), pack2(x[2], x[3], bf16));
+}
+
 // max that keeps a NaN, so that a head holding one gets a NaN scale instead
 // of losing it.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -84,25 +93,16 @@ __device__ __forceinline__ uint32_t int8_code(float y) {
     return (uint32_t)(uint8_t)(int8_t)fminf(fmaxf(roundf(y), -127.f), 127.f);
 }
 
-// Eight 8-bit codes of x / scale, the quotient taken as x times 1 / scale (a
+// Four 8-bit codes of x / scale, the quotient taken as x times 1 / scale (a
 // division an element was a third of the kernel's instructions).
 template <int FMT>
-__device__ __forceinline__ uint2 pack8_8(const float (&x)[8], float inv) {
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        float y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = x[4 * i + j] * inv;
-        if constexpr (FMT == QWEN2_KV_INT8) {
-            w[i] = int8_code(y[0]) | int8_code(y[1]) << 8 | int8_code(y[2]) << 16 | int8_code(y[3]) << 24;
-        } else {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
-            w[i] = lo | hi << 16;
-        }
-    }
-    return make_uint2(w[0], w[1]);
+__device__ __forceinline__ uint32_t pack4_8(const float* x, float inv) {
+    const float y[4] = {x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv};
+    if constexpr (FMT == QWEN2_KV_INT8)
+        return int8_code(y[0]) | int8_code(y[1]) << 8 | int8_code(y[2]) << 16 | int8_code(y[3]) << 24;
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
 }
 
 // The sequence that holds `row`: the number of sequences that end at or before
@@ -137,6 +137,13 @@ struct WriteArgs {
     int out_bf16;
 };
 
+// A pair turned by an angle's (cos, sin).
+__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
+    const float t = fmaf(x, c, -__fmul_rn(y, s));
+    y = fmaf(y, c, __fmul_rn(x, s));
+    x = t;
+}
+
 template <int N>
 struct Int {
     static constexpr int value = N;
@@ -145,7 +152,7 @@ struct Int {
 // One warp per (row, slice of its heads): a row's lookups and rotation factors
 // are loaded once and serve all its heads.
 template <int DT, int FMT, int HD>
-__global__ void __launch_bounds__(kRowThreads) k_paged_write(const __grid_constant__ WriteArgs a) {
+__global__ void __launch_bounds__(kRowThreads, 6) k_paged_write(const __grid_constant__ WriteArgs a) {
     constexpr int kLanes = HD / 8;            // lanes per head
     constexpr int kHeads = 32 / kLanes;       // heads per warp step
     constexpr int kIn = DT == QWEN2_DTYPE_F32 ? 4 : 2;
@@ -176,41 +183,28 @@ __global__ void __launch_bounds__(kRowThreads) k_paged_write(const __grid_consta
     const int off = pos & ((1 << a.kv.page_shift) - 1);
     const int c = lane % kLanes, sub = lane / kLanes;
 
-    // This lane's 8 dims' rotation factors: turned[e] = x[e] * cs[e] + partner[e] * sn[e].
-    float cs[8], sn[8];
-    int partner = lane;
+    // This lane's dims: d0 .. d0 + 3 and d1 .. d1 + 3, and the rotation of its four
+    // pairs: (x[e], x[4 + e]) or, interleaved, (x[2 e], x[2 e + 1]).
+    const int half = a.rotary >> 1;
+    const bool split = !a.interleaved && 4 * c < half;          // a lane of the turning dims, half layout
+    const bool turns = a.interleaved ? 8 * c < a.rotary : split;
+    const int d0 = split ? 4 * c : 8 * c;
+    const int d1 = split ? half + 4 * c : d0 + 4;
+    float cs[4], sn[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 4; ++e) {
         cs[e] = 1.f;
         sn[e] = 0.f;
     }
-    const bool turns = 8 * c < a.rotary;
     if (turns) {
-        const float* t = a.rope + (long long)pos * a.rotary;
-        if (a.interleaved) {
+        const float4* t = reinterpret_cast<const float4*>(a.rope + (long long)pos * a.rotary + 8 * c);
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(t + 8 * c) + p);
-                cs[4 * p] = cs[4 * p + 1] = f.x;
-                sn[4 * p] = -f.y;
-                sn[4 * p + 1] = f.y;
-                cs[4 * p + 2] = cs[4 * p + 3] = f.z;
-                sn[4 * p + 2] = -f.w;
-                sn[4 * p + 3] = f.w;
-            }
-        } else {
-            const int half = a.rotary >> 4;   // lanes of half the turning dims
-            const bool hi = c >= half;
-            const float4* f4 = reinterpret_cast<const float4*>(t + 16 * (hi ? c - half : c));
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const float4 f = __ldg(f4 + p);
-                cs[2 * p] = f.x;
-                sn[2 * p] = hi ? f.y : -f.y;
-                cs[2 * p + 1] = f.z;
-                sn[2 * p + 1] = hi ? f.w : -f.w;
-            }
-            partner = hi ? lane - half : lane + half;
+        for (int p = 0; p < 2; ++p) {
+            const float4 f = __ldg(t + p);
+            cs[2 * p] = f.x;
+            sn[2 * p] = f.y;
+            cs[2 * p + 1] = f.z;
+            sn[2 * p + 1] = f.w;
         }
     }
     const long long kv_row = (long long)page * a.kv.page_bytes + (long long)off * a.kv.token_bytes;
@@ -220,29 +214,31 @@ __global__ void __launch_bounds__(kRowThreads) k_paged_write(const __grid_consta
         constexpr int kKind = decltype(kind)::value;
         constexpr int kBatch = kKind == 0 ? 4 : 2;
         const Rows& src = kKind == 0 ? a.q : kKind == 1 ? a.k : a.v;
-        const char* from = src.data + (long long)row * src.row_bytes + 8 * kIn * c;
+        const char* from = src.data + (long long)row * src.row_bytes;
         const float* nw = kKind == 0 ? a.q_norm : kKind == 1 ? a.k_norm : nullptr;
         float w[8];
         if (kKind != 2 && nw) {
-            const float4 w0 = __ldg(reinterpret_cast<const float4*>(nw + 8 * c));
-            const float4 w1 = __ldg(reinterpret_cast<const float4*>(nw + 8 * c) + 1);
+            const float4 w0 = __ldg(reinterpret_cast<const float4*>(nw + d0));
+            const float4 w1 = __ldg(reinterpret_cast<const float4*>(nw + d1));
             w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
             w[4] = w1.x; w[5] = w1.y; w[6] = w1.z; w[7] = w1.w;
         }
         for (; h0 < h1; h0 += kBatch * kHeads) {
-            Raw8<DT> raw[kBatch];
+            Raw4<DT> raw[kBatch][2];
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
-                const int h = h0 + b * kHeads + sub;
-                raw[b] = Raw8<DT>{};
-                if (h < h1) raw[b] = load8<DT>(from + (long long)h * src.head_bytes);
+                const int h = min(h0 + b * kHeads + sub, h1 - 1);    // past the last head: its values, not stored
+                const char* p = from + (long long)h * src.head_bytes;
+                raw[b][0] = load4<DT>(p + kIn * d0);
+                raw[b][1] = load4<DT>(p + kIn * d1);
             }
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
                 if (h0 + b * kHeads >= h1) break;
                 const int h = h0 + b * kHeads + sub;
                 float x[8];
-                to_f32<DT>(raw[b], x);
+                to_f32<DT>(raw[b][0], x);
+                to_f32<DT>(raw[b][1], x + 4);
                 if (kKind != 2 && nw) {
                     float ss = 0.f;
 #pragma unroll
@@ -254,27 +250,27 @@ __global__ void __launch_bounds__(kRowThreads) k_paged_write(const __grid_consta
                     for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
                 }
                 if (kKind != 2 && a.rotary) {
-                    float p[8];
                     if (a.interleaved) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
+                        for (int e = 0; e < 4; ++e) turn(x[2 * e], x[2 * e + 1], cs[e], sn[e]);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, x[e], partner);
-                    }
-                    if (turns) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], cs[e], __fmul_rn(p[e], sn[e]));
+                        for (int e = 0; e < 4; ++e) turn(x[e], x[4 + e], cs[e], sn[e]);
                     }
                 }
                 if constexpr (kKind == 0) {
-                    if (h < h1)
-                        *reinterpret_cast<uint4*>(a.q_out.data + (long long)row * a.q_out.row_bytes +
-                                                  (long long)h * a.q_out.head_bytes + 16 * c) = pack8_16(x, a.out_bf16);
+                    if (h < h1) {
+                        char* dst = a.q_out.data + (long long)row * a.q_out.row_bytes + (long long)h * a.q_out.head_bytes;
+                        *reinterpret_cast<uint2*>(dst + 2 * d0) = pack4_16(x, a.out_bf16);
+                        *reinterpret_cast<uint2*>(dst + 2 * d1) = pack4_16(x + 4, a.out_bf16);
+                    }
                 } else {
                     char* dst = (kKind == 1 ? a.kv.k : a.kv.v) + kv_row + (long long)h * a.kv.head_bytes;
                     if constexpr (FMT == QWEN2_KV_F16 || FMT == QWEN2_KV_BF16) {
-                        if (h < h1) *reinterpret_cast<uint4*>(dst + 16 * c) = pack8_16(x, FMT == QWEN2_KV_BF16);
+                        if (h < h1) {
+                            *reinterpret_cast<uint2*>(dst + 2 * d0) = pack4_16(x, FMT == QWEN2_KV_BF16);
+                            *reinterpret_cast<uint2*>(dst + 2 * d1) = pack4_16(x + 4, FMT == QWEN2_KV_BF16);
+                        }
                     } else {
                         float m = 0.f;
 #pragma unroll
@@ -283,7 +279,9 @@ __global__ void __launch_bounds__(kRowThreads) k_paged_write(const __grid_consta
                         for (int o = kLanes / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
                         const float scale = m == 0.f ? 1.f : __fdiv_rn(m, FMT == QWEN2_KV_INT8 ? 127.f : 448.f);
                         if (h < h1) {
-                            *reinterpret_cast<uint2*>(dst + 8 * c) = pack8_8<FMT>(x, __fdiv_rn(1.f, scale));
+                            const float inv = __fdiv_rn(1.f, scale);
+                            *reinterpret_cast<uint32_t*>(dst + d0) = pack4_8<FMT>(x, inv);
+                            *reinterpret_cast<uint32_t*>(dst + d1) = pack4_8<FMT>(x + 4, inv);
                             if (c == 0)
                                 (kKind == 1 ? a.kv.k_scale
                                             : a.kv.v_scale)[(((long long)page * a.kv.n_kv + h) << a.kv.page_shift) + off] = scale;
@@ -293,18 +291,12 @@ __global__ void __launch_bounds__(kRowThreads) k_paged_write(const __grid_consta
             }
         }
     };
-    // One warp per row: all its heads.  Otherwise its share of the steps.
+    // This warp's share of the row's steps.
     const int sq = (a.n_head + kHeads - 1) / kHeads, sk = (a.kv.n_kv + kHeads - 1) / kHeads;
-    const bool whole = a.slices == 1;
-    for (int i = slice; i < (whole ? 3 : sq + 2 * sk); i += a.slices) {
-        const int kind = whole ? i : i < sq ? 0 : i < sq + sk ? 1 : 2;
-        const int n = kind == 0 ? a.n_head : a.kv.n_kv;
-        const int h0 = whole ? 0 : kHeads * (kind == 0 ? i : kind == 1 ? i - sq : i - sq - sk);
-        const int h1 = whole ? n : min(n, h0 + kHeads);
-        if (kind == 0) heads(Int<0>{}, h0, h1);
-        else if (kind == 1) heads(Int<1>{}, h0, h1);
-        else heads(Int<2>{}, h0, h1);
-    }
+    const int s0 = (sq + 2 * sk) * slice / a.slices, s1 = (sq + 2 * sk) * (slice + 1) / a.slices;
+    heads(Int<0>{}, kHeads * s0, min(a.n_head, kHeads * s1));
+    heads(Int<1>{}, kHeads * max(0, s0 - sq), min(a.kv.n_kv, kHeads * (s1 - sq)));
+    heads(Int<2>{}, kHeads * max(0, s0 - sq - sk), min(a.kv.n_kv, kHeads * (s1 - sq - sk)));
 }
 
 struct ReadArgs {
@@ -478,13 +470,15 @@ cudaError_t enqueue_write(const Pool& kv, const Batch& b, const qwen2_paged_writ
         a.rotary = o->rope ? o->rotary_dim : 0;
         a.interleaved = o->interleaved;
     }
-    // One warp per row once the rows alone fill the device, so that a row's
-    // lookups are made once; with fewer rows its heads are spread over as many
-    // warps as do, down to one step of heads each (a decode step's few rows are
-    // then one round of loads).
+    // One warp per row once the rows alone fill the device (12 warps an SM),
+    // so that a row's lookups are made once; with fewer rows its heads are
+    // spread over as many warps as do, down to one step of heads each (a decode
+    // step's few rows are then one round of loads).  2,326 rows of 28 + 2 x 4
+    // heads of 128 into int8 take 18.6 us so, 21.3 us with 16 and 22.2 us with
+    // 48 warps an SM wanted; 152 rows take the same with any.
     const int heads = head_dim == 64 ? 4 : 2;
     const int steps = (n_head + heads - 1) / heads + 2 * ((kv.n_kv + heads - 1) / heads);
-    a.slices = b.n_rows >= 152 * 8 ? 1 : min(steps, (152 * 24 + b.n_rows - 1) / b.n_rows);
+    a.slices = (int)min((long long)steps, (152 * 12 + (long long)b.n_rows - 1) / b.n_rows);
     switch (dtype) {
         case QWEN2_DTYPE_F32: return launch_write_fmt<QWEN2_DTYPE_F32>(a, format, head_dim, st);
         case QWEN2_DTYPE_F16: return launch_write_fmt<QWEN2_DTYPE_F16>(a, format, head_dim, st);
