@@ -54,7 +54,7 @@ struct Shape {
     static constexpr int kTile = kStep * kRowBytes;                // K or V of a step
     static constexpr int kScales = K == kSame16 ? 0 : 2 * kStep * 4;
     static constexpr int kStage = 2 * kTile + kScales;
-    static constexpr int kStages = kTile <= 1024 ? 6 : kTile <= 2048 ? 4 : 3;
+    static constexpr int kStages = kTile <= 1024 ? 6 : kTile <= 2048 && K == kSame16 ? 4 : 3;
     static constexpr int kRing = kStage * kStages;                 // per warp
 };
 
@@ -193,6 +193,10 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
             return (unsigned)p < (unsigned)a.kv.n_pages ? p : -2;
         };
         unsigned bad = 0;     // per ring stage: its page id was bad
+        // A lane copies piece lane % (RB / 16) of every kRowsAtOnce'th position.
+        constexpr int kRowsAtOnce = 512 / RB;
+        const long long lane_src = (long long)(lane / (RB / 16)) * a.kv.token_bytes + 16 * (lane % (RB / 16));
+        const long long row_step = kRowsAtOnce * a.kv.token_bytes;
         // Issues the copies of the feed's step into `stage` and moves it on.
         auto issue = [&](int stage) {
             bad &= ~(1u << stage);
@@ -203,14 +207,17 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
                 const long long at = (long long)f_page * a.kv.page_bytes + (long long)off * a.kv.token_bytes +
                                      (long long)f.t.head * a.kv.head_bytes;
                 const uint32_t dst = ring + stage * S::kStage;
+                // Positions past n are not read, though their page's memory is there.
+                const char* ks = a.kv.k + at + lane_src;
+                const char* vs = a.kv.v + at + lane_src;
 #pragma unroll
                 for (int i = 0; i < RB / 32; ++i) {
-                    const int e = lane + 32 * i, r = e / (RB / 16), c = e % (RB / 16);
-                    const bool in = r < n;
-                    const long long src = at + (long long)(in ? r : 0) * a.kv.token_bytes + 16 * c;
-                    const uint32_t d = dst + r * RB + 16 * swz<RB>(r, c);
-                    cp16(d, a.kv.k + src, in);
-                    cp16(d + S::kTile, a.kv.v + src, in);
+                    const int r = lane / (RB / 16) + i * kRowsAtOnce;
+                    const uint32_t d = dst + r * RB + 16 * swz<RB>(r, lane % (RB / 16));
+                    cp16(d, ks, r < n);
+                    cp16(d + S::kTile, vs, r < n);
+                    ks += row_step;
+                    vs += row_step;
                 }
                 if constexpr (k8) {
                     if (lane < 8) {
