@@ -130,14 +130,23 @@ struct Tile {
     int u0, n;               // first unit and number of units of this CTA's part; n <= 0: past its end
 };
 
-// Sums of the slots of the first s sequences, and the CTA's share.
+// a / b of non-negative numbers; a division of 64 bits is some 100 dependent
+// instructions, and the work list's numbers rarely need one (a call, to keep
+// it out of the kernels' instruction cache lines).
+static __device__ __noinline__ long long div_long(long long a, long long b) { return a / b; }
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return div_long(a, b);
+}
+
+// Slots of one kv head of the first s sequences, and the CTA's share.
 struct WorkList {
     const long long* prefix;   // shared memory [n_seq + 1]
     long long begin, end;      // this CTA's slots
     long long each, rest;      // the first `rest` CTAs take each + 1 slots, the others `each`
     __device__ __forceinline__ int owner(long long slot) const {
         const long long big = rest * (each + 1);
-        return (int)(slot < big ? slot / (each + 1) : rest + (slot - big) / each);
+        return (int)(slot < big ? div_pos(slot, each + 1) : rest + div_pos(slot - big, each));
     }
 };
 
@@ -146,64 +155,80 @@ __device__ __forceinline__ bool owns(const AttnArgs& a, const Seq& q) {
     return packed > a.rows_lo && packed <= a.rows_hi;
 }
 
-// Builds the prefix sums with the whole block (at most 4096 sequences) and
-// returns this CTA's share.  A CTA gets at least min_slots > kCost slots, so
-// that small batches are not cut finer than pays and every part has a unit.
-template <int kKeys, int kCost>
-__device__ __forceinline__ WorkList build_work(const AttnArgs& a, long long* prefix, int min_slots) {
-    // A thread per sequence; one with many causal tiles (each of its own length)
-    // is left to a whole warp.
-    for (int s = threadIdx.x; s < a.b.n_seq; s += blockDim.x) {
-        const Seq q = load_seq(a.b, a.kv.page_shift, s);
-        if (blockIdx.x == 0 && (q.bad_rows || q.bad_len))
-            raise_guard(a.b.guard, q.bad_rows ? kGuardShape : kGuardPosition);
+// Builds the prefix sums with the whole block (at most 4096 sequences and 32
+// warps, at least 4) and returns this CTA's share.  A CTA gets at least
+// kMin > kCost slots, so that small batches are not cut finer than pays and
+// every part has a unit.  A warp takes 32 sequences at a time; up to 32 need a
+// single barrier.
+template <int kKeys, int kCost, int kMin>
+__device__ __forceinline__ WorkList build_work(const AttnArgs& a, long long* prefix) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+#pragma unroll 1
+    for (int s0 = 32 * warp; s0 < a.b.n_seq; s0 += 32 * warps) {
+        const int s = s0 + lane;
         long long u = 0;
-        if (owns(a, q)) {
-            const int tiles = (q.n * a.group + a.tile - 1) / a.tile;
-            if (!a.causal) u = (long long)tiles * (kCost + tile_units<kKeys>(q, a.group, 0, a.tile, false));
-            else if (tiles <= 4)
-                for (int t = 0; t < tiles; ++t) u += kCost + tile_units<kKeys>(q, a.group, t, a.tile, true);
-            else u = -1;
-        }
-        prefix[s + 1] = u < 0 ? u : u * a.kv.n_kv;
-    }
-    __syncthreads();
-    for (int s = threadIdx.x >> 5; s < a.b.n_seq; s += blockDim.x >> 5) {
-        if (prefix[s + 1] >= 0) continue;
-        const Seq q = load_seq(a.b, a.kv.page_shift, s);
-        const int tiles = (q.n * a.group + a.tile - 1) / a.tile;
-        long long u = 0;
-        for (int t = threadIdx.x & 31; t < tiles; t += 32) u += kCost + tile_units<kKeys>(q, a.group, t, a.tile, true);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-        if ((threadIdx.x & 31) == 0) prefix[s + 1] = u * a.kv.n_kv;
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        long long carry = 0;
-        for (int s0 = 0; s0 < a.b.n_seq; s0 += 32) {
-            const int s = s0 + threadIdx.x;
-            long long v = s < a.b.n_seq ? prefix[s + 1] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(0xffffffffu, v, o);
-                if ((int)threadIdx.x >= o) v += u;
+        Seq q{};
+        bool many = false;
+        if (s < a.b.n_seq) {
+            q = load_seq(a.b, a.kv.page_shift, s);
+            if (blockIdx.x == 0 && (q.bad_rows || q.bad_len))
+                raise_guard(a.b.guard, q.bad_rows ? kGuardShape : kGuardPosition);
+            if (owns(a, q)) {
+                const int tiles = (q.n * a.group + a.tile - 1) / a.tile;
+                many = a.causal && tiles > 1;
+                u = (long long)tiles * (kCost + tile_units<kKeys>(q, a.group, 0, a.tile, a.causal));
             }
-            v += carry;
-            if (s < a.b.n_seq) prefix[s + 1] = v;
-            carry = __shfl_sync(0xffffffffu, v, 31);
         }
-        if (threadIdx.x == 0) prefix[0] = 0;
+        // Causal tiles each have a length of their own: the whole warp counts them.
+        for (unsigned left = __ballot_sync(0xffffffffu, many); left; left &= left - 1) {
+            const int src = __ffs(left) - 1;
+            Seq w{};
+            w.n = __shfl_sync(0xffffffffu, q.n, src);
+            w.kv = __shfl_sync(0xffffffffu, q.kv, src);
+            const int tiles = (w.n * a.group + a.tile - 1) / a.tile;
+            long long sum = 0;
+            for (int t = lane; t < tiles; t += 32) sum += kCost + tile_units<kKeys>(w, a.group, t, a.tile, true);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == src) u = sum;
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, u, o);
+            if (lane >= o) u += v;
+        }
+        if (s < a.b.n_seq) prefix[s + 1] = u;
     }
+    if (threadIdx.x == 0) prefix[0] = 0;
     __syncthreads();
-    const long long total = prefix[a.b.n_seq];
-    const long long most = total / min_slots;
+    if (a.b.n_seq > 32) {
+        // Each 32's sums are their own so far: lane k holds what comes before
+        // the warp's k-th 32.
+        long long before = 0;
+        int k = 0;
+        for (int s0 = 32 * warp; s0 < a.b.n_seq; s0 += 32 * warps, ++k) {
+            long long sum = 0;
+            for (int c = 32 * (lane + 1); c <= s0; c += 1024) sum += prefix[c];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == k) before = sum;
+        }
+        __syncthreads();
+        k = 0;
+        for (int s0 = 32 * warp; s0 < a.b.n_seq; s0 += 32 * warps, ++k) {
+            const long long add = __shfl_sync(0xffffffffu, before, k);
+            if (s0 + lane < a.b.n_seq) prefix[s0 + lane + 1] += add;
+        }
+        __syncthreads();
+    }
+    const long long total = prefix[a.b.n_seq] * a.kv.n_kv;
+    const long long most = (long long)((unsigned long long)total / kMin);
     const long long g = most < (long long)gridDim.x ? (most > 0 ? most : 1) : (long long)gridDim.x;
     WorkList w;
     w.prefix = prefix;
     const long long c = blockIdx.x;
     // total / g and the remainder keep the products within 64 bits.
-    w.each = total / g;
+    w.each = div_pos(total, g);
     w.rest = total - w.each * g;
     w.begin = c < g ? w.each * c + (c < w.rest ? c : w.rest) : total;
     w.end = c < g ? w.begin + w.each + (c < w.rest ? 1 : 0) : total;
@@ -221,23 +246,23 @@ __device__ __forceinline__ void set_part(const WorkList& w, Tile& t) {
 // that is not empty.
 template <int kKeys, int kCost>
 __device__ __forceinline__ Tile find_tile(const AttnArgs& a, const WorkList& w) {
-    int lo = 0, hi = a.b.n_seq;          // largest s with prefix[s] <= begin: it has slots of its own
+    int lo = 0, hi = a.b.n_seq;          // the largest s that begins at or before it has slots of its own
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (w.prefix[mid] <= w.begin) lo = mid;
+        if (w.prefix[mid] * a.kv.n_kv <= w.begin) lo = mid;
         else hi = mid;
     }
     Tile t;
     t.s = lo;
     t.q = load_seq(a.b, a.kv.page_shift, lo);
-    const long long per_head = (w.prefix[lo + 1] - w.prefix[lo]) / a.kv.n_kv;
-    long long r = w.begin - w.prefix[lo];
-    t.head = (int)(r / per_head);
+    const long long per_head = w.prefix[lo + 1] - w.prefix[lo];
+    long long r = w.begin - w.prefix[lo] * a.kv.n_kv;
+    t.head = (int)div_pos(r, per_head);
     r -= t.head * per_head;
     const int tiles = (t.q.n * a.group + a.tile - 1) / a.tile;
     if (!a.causal) {
         const int slots = kCost + tile_units<kKeys>(t.q, a.group, 0, a.tile, false);
-        t.t = (int)(r / slots);
+        t.t = (int)div_pos(r, slots);
         r -= (long long)t.t * slots;
     } else {
         // 32 tiles at a time: the first one whose slots reach past r.

@@ -54,14 +54,26 @@ struct Shape {
     static constexpr int kTile = kStep * kRowBytes;                // K or V of a step
     static constexpr int kScales = K == kSame16 ? 0 : 2 * kStep * 4;
     static constexpr int kStage = 2 * kTile + kScales;
-    static constexpr int kStages = kTile <= 1024 ? 6 : kTile <= 2048 && K == kSame16 ? 4 : 3;
+    static constexpr int kStages = kTile <= 1024 ? 6 : 3;
     static constexpr int kRing = kStage * kStages;                 // per warp
 };
 
+// Row tiles come in three forms: MT = 1 or 2 keeps 16 MT rows in the products'
+// M (scores rows x positions), MT = 0 keeps 8 rows in N (scores positions x
+// rows): half the products and half the softmax of a 16-row tile.
+template <int MT>
+constexpr int rows_of = MT ? 16 * MT : 8;
+// CTAs an SM that the registers are held down to.
+template <int MT>
+constexpr int ctas_of = MT == 0 ? 4 : MT == 1 ? 3 : 2;
+
 template <int HD, int MT>
 struct Meet {   // where the warps meet
-    float o[16 * MT][HD + 4];
-    float m[kWarps][16 * MT], l[kWarps][16 * MT], g[kWarps];
+    // Two n tiles' 16 dims stand as 4 dims a lane of a quad (MT > 0), or the dims
+    // g and g + 8 of an m tile side by side (MT = 0); the padding puts the rows
+    // of one access into different banks.
+    float o[rows_of<MT>][HD + (MT ? 16 : 4)];
+    float m[kWarps][rows_of<MT>], l[kWarps][rows_of<MT>], g[kWarps];
 };
 
 // 16-byte piece c of position r stands at piece c ^ f(r) of its row, so that
@@ -110,6 +122,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The transpose of an 8 x 8 matrix of 16-bit elements across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     if constexpr (BF16) {
@@ -147,6 +166,18 @@ __device__ __forceinline__ float quad_sum(float v) {
     return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
+// Over the lanes of equal lane % 4.
+__device__ __forceinline__ float col_max(float v) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float col_sum(float v) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 // The power of two at or above v, as an exponent in [-100, 100].
 __device__ __forceinline__ int ceil_log2(float v) {
     const int b = __float_as_int(v);
@@ -163,11 +194,12 @@ struct Feed {
 };
 
 template <int HD, Kind K, bool BF16, int MT>
-__global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, ctas_of<MT>) k_paged_attn(const __grid_constant__ AttnArgs a) {
     using S = Shape<HD, K>;
     constexpr bool k8 = K != kSame16;
     constexpr bool kMmaBf16 = BF16 && !k8;
-    constexpr int kRows = 16 * MT;
+    constexpr bool kCols = MT == 0;              // rows in N
+    constexpr int kRows = rows_of<MT>, kM = kCols ? 1 : MT, kH = kCols ? 1 : 2;
     constexpr int RB = S::kRowBytes;
     extern __shared__ __align__(128) unsigned char smem[];
     Meet<HD, MT>& meet = *reinterpret_cast<Meet<HD, MT>*>(smem);
@@ -177,17 +209,17 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t4 = lane & 3;
-    const WorkList work = build_work<kUnit, kCost>(a, prefix, kCost + 1);
+    const WorkList work = build_work<kUnit, kCost, kCost + 1>(a, prefix);
     bool open = false;
     if (work.begin < work.end) {
         const uint32_t ring = (uint32_t)__cvta_generic_to_shared(rings + warp * S::kRing);
         Tile t = find_tile<kUnit, kCost>(a, work);
         Feed f{t, 0};
         int f_page = -1;
-        // Page of the feed's current step; -1 if it has no keys, -2 if its id is bad.
-        auto look_up = [&]() -> int {
-            if (f.t.n <= 0) return -1;
-            const int key0 = (f.t.u0 + f.i) * kUnit + warp * kStep;
+        // Page of a step of the feed's tile; -1 if it has no keys, -2 if its id is bad.
+        auto look_up = [&](int i) -> int {
+            if (i >= f.t.n) return -1;
+            const int key0 = (f.t.u0 + i) * kUnit + warp * kStep;
             if (key0 >= f.t.keys) return -1;
             const int p = __ldg(a.b.pages + (long long)f.t.s * a.b.pages_stride + (key0 >> a.kv.page_shift));
             return (unsigned)p < (unsigned)a.kv.n_pages ? p : -2;
@@ -236,23 +268,24 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
                 f.i = 0;
                 next_tile<kUnit, kCost>(a, work, f.t);
             }
-            f_page = look_up();
         };
-        f_page = look_up();
-#pragma unroll 1
-        for (int st = 0; st < S::kStages - 1; ++st) issue(st);
+        // The pages of the first steps come in one load, a lane each.
+        const int first_pages = look_up(lane);
+        const int first_n = t.n;
+        bool begun = false;
         int stage = 0;
 
         for (;;) {
             // ---- a tile's part: queries ------------------------------------------
             const int packed0 = t.t * kRows, packed = t.q.n * a.group;
-            uint32_t qf[MT][HD / 16][4];
-            float rs[MT][2];           // factor of a row's scores
-            int lim[MT][2];            // last position a row sees
+            uint32_t qf[kM][HD / 16][4];
+            float rs[kM][2];           // factor of a row's scores
+            int lim[kM][2];            // last position a row sees
+            uint4 w[kM][kH][k8 ? HD / 32 : 1];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < kM; ++mt)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < kH; ++h) {
                     const int i = packed0 + 16 * mt + 8 * h + g;
                     const bool in = i < packed;
                     const int row = t.q.q0 + (in ? i / a.group : 0), qh = t.head * a.group + (in ? i % a.group : 0);
@@ -268,19 +301,37 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
                     } else {
                         // Dims in the order the codes are read in: 4 codes of a word
                         // make the two halves of a k step's pairs.
-                        uint4 w[HD / 32];
 #pragma unroll
                         for (int b = 0; b < HD / 64; ++b)
 #pragma unroll
                             for (int j = 0; j < 2; ++j)
-                                w[2 * b + j] = in ? __ldg(reinterpret_cast<const uint4*>(src + 128 * b + 32 * t4 + 16 * j))
-                                                  : make_uint4(0, 0, 0, 0);
+                                w[mt][h][2 * b + j] =
+                                    in ? __ldg(reinterpret_cast<const uint4*>(src + 128 * b + 32 * t4 + 16 * j))
+                                       : make_uint4(0, 0, 0, 0);
+                    }
+                }
+            // The first copies go out while the first queries come in.
+            if (!begun) {
+                begun = true;
+#pragma unroll 1
+                for (int st = 0; st < S::kStages - 1; ++st) {
+                    f_page = st < first_n ? __shfl_sync(0xffffffffu, first_pages, st) : look_up(f.i);
+                    issue(st);
+                }
+                f_page = look_up(f.i);
+            }
+            if constexpr (k8) {
+#pragma unroll
+                for (int mt = 0; mt < kM; ++mt)
+#pragma unroll
+                    for (int h = 0; h < kH; ++h) {
+                        uint4(&w1)[HD / 32] = w[mt][h];
                         if constexpr (BF16) {
                             float big = 0.f;
                             float x[HD / 4];
 #pragma unroll
                             for (int j = 0; j < HD / 32; ++j) {
-                                const uint32_t u[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+                                const uint32_t u[4] = {w1[j].x, w1[j].y, w1[j].z, w1[j].w};
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     x[8 * j + 2 * e] = __uint_as_float(u[e] << 16);
@@ -293,28 +344,40 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
                             rs[mt][h] *= pow2i(e2);
 #pragma unroll
                             for (int j = 0; j < HD / 32; ++j)
-                                w[j] = make_uint4(pack2<false>(x[8 * j] * down, x[8 * j + 1] * down),
-                                                  pack2<false>(x[8 * j + 2] * down, x[8 * j + 3] * down),
-                                                  pack2<false>(x[8 * j + 4] * down, x[8 * j + 5] * down),
-                                                  pack2<false>(x[8 * j + 6] * down, x[8 * j + 7] * down));
+                                w1[j] = make_uint4(pack2<false>(x[8 * j] * down, x[8 * j + 1] * down),
+                                                   pack2<false>(x[8 * j + 2] * down, x[8 * j + 3] * down),
+                                                   pack2<false>(x[8 * j + 4] * down, x[8 * j + 5] * down),
+                                                   pack2<false>(x[8 * j + 6] * down, x[8 * j + 7] * down));
                         }
 #pragma unroll
                         for (int j = 0; j < HD / 32; ++j) {
-                            qf[mt][2 * j][h] = w[j].x;
-                            qf[mt][2 * j][2 + h] = w[j].y;
-                            qf[mt][2 * j + 1][h] = w[j].z;
-                            qf[mt][2 * j + 1][2 + h] = w[j].w;
+                            qf[mt][2 * j][h] = w1[j].x;
+                            qf[mt][2 * j][2 + h] = w1[j].y;
+                            qf[mt][2 * j + 1][h] = w1[j].z;
+                            qf[mt][2 * j + 1][2 + h] = w1[j].w;
                         }
                     }
+            }
+            if constexpr (kCols) {
+                // The lane's scores are of rows 2 t4 and 2 t4 + 1.
+                const float r = rs[0][0];
+                const int last = lim[0][0];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    rs[0][j] = __shfl_sync(0xffffffffu, r, 8 * t4 + 4 * j);
+                    lim[0][j] = __shfl_sync(0xffffffffu, last, 8 * t4 + 4 * j);
                 }
+            }
+            const bool upper = packed - packed0 > kRows - 8;   // the last 8 rows hold any
             const int sure = row_limit(a, t.q, packed0);   // every row of the tile sees positions up to here
-            float o[MT][HD / 8][4];
-            float m[MT][2], l[MT][2];
+            constexpr int kTiles = kCols ? HD / 16 : HD / 8;
+            float o[kM][kTiles][4];
+            float m[kM][2], l[kM][2];
             int ge = -100;             // exponent of G
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
+            for (int mt = 0; mt < kM; ++mt) {
 #pragma unroll
-                for (int d = 0; d < HD / 8; ++d)
+                for (int d = 0; d < kTiles; ++d)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[mt][d][e] = 0.f;
                 m[mt][0] = m[mt][1] = -INFINITY;
@@ -326,10 +389,124 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
                 __syncwarp();
                 // The stage that the step before this one emptied is filled again.
                 issue(stage == 0 ? S::kStages - 1 : stage - 1);
+                f_page = look_up(f.i);
                 const int key0 = (t.u0 + i) * kUnit + warp * kStep;
                 const uint32_t kt = ring + stage * S::kStage, vt = kt + S::kTile;
                 const bool skip = key0 >= t.keys || (bad >> stage & 1);
-                if (!skip) {
+                if constexpr (kCols) {
+                    if (!skip) {
+                        const bool cut = key0 + kStep - 1 > sure || key0 + kStep > t.keys;
+                        // scores: positions g and g + 8 of rows 2 t4 and 2 t4 + 1, in two chains
+                        float c[2][4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) c[0][e] = c[1][e] = 0.f;
+                        const int r = (lane & 7) + ((lane >> 3) & 1) * 8, hi = lane >> 4;
+                        if constexpr (!k8) {
+#pragma unroll
+                            for (int k = 0; k < HD / 16; ++k) {
+                                uint32_t b[4];
+                                ldsm4(kt + r * RB + 16 * swz<RB>(r, 2 * k + hi), b);
+                                mma16816<kMmaBf16>(c[k & 1], b, qf[0][k][0], qf[0][k][2]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int b = 0; b < HD / 64; ++b) {
+                                uint32_t x[2][4];
+#pragma unroll
+                                for (int n = 0; n < 2; ++n)
+                                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                                 : "=r"(x[n][0]), "=r"(x[n][1]), "=r"(x[n][2]), "=r"(x[n][3])
+                                                 : "r"(kt + (8 * n + g) * RB + 16 * swz<RB>(8 * n + g, 4 * b + t4))
+                                                 : "memory");
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const uint32_t f[4] = {codes2<K, 0, 1>(x[0][k]), codes2<K, 0, 1>(x[1][k]),
+                                                           codes2<K, 2, 1>(x[0][k]), codes2<K, 2, 1>(x[1][k])};
+                                    mma16816<false>(c[k & 1], f, qf[0][4 * b + k][0], qf[0][4 * b + k][2]);
+                                }
+                            }
+                        }
+                        float v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = (c[0][e] + c[1][e]) * rs[0][e & 1];
+                        float vs[2];
+                        if constexpr (k8) {
+                            float ks[2], top = 0.f;
+#pragma unroll
+                            for (int n = 0; n < 2; ++n) {
+                                const uint32_t sa = kt + 2 * S::kTile + 4 * (8 * n + g);
+                                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks[n]) : "r"(sa) : "memory");
+                                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs[n]) : "r"(sa + 64) : "memory");
+                                // Positions that are no keys: whatever stands in the pool there is left out.
+                                if (key0 + 8 * n + g >= t.keys) vs[n] = 0.f;
+                                top = fmaxf(top, vs[n]);
+                                v[2 * n] *= ks[n];
+                                v[2 * n + 1] *= ks[n];
+                            }
+                            // A larger scale than G (the lane's own copy) moves it, in the whole warp.
+                            if (__any_sync(0xffffffffu, ceil_log2(top) > ge)) {
+                                const int ne = max(ge, ceil_log2(col_max(top)));
+                                const float down = pow2i(max(ge - ne, -126));
+#pragma unroll
+                                for (int d = 0; d < kTiles; ++d)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) o[0][d][e] *= down;
+                                ge = ne;
+                            }
+                            const float inv = pow2i(-ge);
+                            vs[0] *= inv;
+                            vs[1] *= inv;
+                        }
+                        if (cut) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (key0 + 8 * (e >> 1) + g > min(lim[0][e & 1], t.keys - 1)) v[e] = -INFINITY;
+                        }
+                        float corr[2];
+                        bool moved = false;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float mn = fmaxf(m[0][j], col_max(fmaxf(v[j], v[2 + j])));
+                            const float base = mn == -INFINITY ? 0.f : mn;
+                            moved |= mn != m[0][j];
+                            corr[j] = ex2(m[0][j] - base);
+                            m[0][j] = mn;
+                            v[j] = ex2(v[j] - base);
+                            v[2 + j] = ex2(v[2 + j] - base);
+                            l[0][j] = fmaf(l[0][j], corr[j], v[j] + v[2 + j]);
+                        }
+                        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                            for (int d = 0; d < kTiles; ++d)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[0][d][e] *= corr[e & 1];
+                        }
+                        if constexpr (k8) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] *= vs[e >> 1];
+                        }
+                        const uint32_t p0 = transpose8(pack2<kMmaBf16>(v[0], v[1]));
+                        const uint32_t p1 = transpose8(pack2<kMmaBf16>(v[2], v[3]));
+                        // values: dims in M, so that the rows stay in N
+#pragma unroll
+                        for (int d = 0; d < RB / 32; ++d) {
+                            uint32_t b[4];
+                            ldsm4t(vt + r * RB + 16 * swz<RB>(r, 2 * d + hi), b);
+                            if constexpr (!k8) {
+                                const uint32_t f[4] = {b[0], b[2], b[1], b[3]};
+                                mma16816<kMmaBf16>(o[0][d], f, p0, p1);
+                            } else {
+                                // A piece is 16 dims: the even ones are rows g, the odd ones rows g + 8.
+#pragma unroll
+                                for (int n = 0; n < 2; ++n) {
+                                    const uint32_t f[4] = {codes2<K, 0, 2>(b[2 * n]), codes2<K, 1, 2>(b[2 * n]),
+                                                           codes2<K, 0, 2>(b[2 * n + 1]), codes2<K, 1, 2>(b[2 * n + 1])};
+                                    mma16816<false>(o[0][2 * d + n], f, p0, p1);
+                                }
+                            }
+                        }
+                    }
+                } else if (!skip) {
                     // scores
                     float s[MT][2][4];
 #pragma unroll
@@ -420,6 +597,11 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
                     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
+                            if (mt == MT - 1 && h == 1 && !upper) {
+                                corr[mt][h] = 1.f;
+                                p[mt][h] = p[mt][2 + h] = 0u;
+                                continue;
+                            }
                             float v[4] = {s[mt][0][2 * h] * rs[mt][h], s[mt][0][2 * h + 1] * rs[mt][h],
                                           s[mt][1][2 * h] * rs[mt][h], s[mt][1][2 * h + 1] * rs[mt][h]};
                             if (cut) {
@@ -487,43 +669,67 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
             }
             // ---- the four warps meet ----------------------------------------------
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < kM; ++mt)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float sum = quad_sum(l[mt][h]);
-                    if (t4 == 0) {
-                        meet.m[warp][16 * mt + 8 * h + g] = m[mt][h];
-                        meet.l[warp][16 * mt + 8 * h + g] = sum;
+                    const float sum = kCols ? col_sum(l[mt][h]) : quad_sum(l[mt][h]);
+                    const int r = kCols ? 2 * t4 + h : 16 * mt + 8 * h + g;
+                    if ((kCols ? g : t4) == 0) {
+                        meet.m[warp][r] = m[mt][h];
+                        meet.l[warp][r] = sum;
                     }
                 }
             __syncthreads();
-            float f_row[MT][2];
+            float f_row[kM][2];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int mt = 0; mt < kM; ++mt)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    const int r = kCols ? 2 * t4 + h : 16 * mt + 8 * h + g;
                     float top = -INFINITY;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, meet.m[w][16 * mt + 8 * h + g]);
+                    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, meet.m[w][r]);
                     f_row[mt][h] = ex2(m[mt][h] - (top == -INFINITY ? 0.f : top));
                     if constexpr (k8) f_row[mt][h] *= pow2i(ge);
                 }
+            // Four turns, in each of which a warp adds a quarter of its dims, another
+            // than the other warps: every element in an order of its own, but a fixed one.
 #pragma unroll 1
-            for (int w = 0; w < kWarps; ++w) {
-                if (warp == w) {
+            for (int turn = 0; turn < kWarps; ++turn) {
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
+                for (int d = 0; d < kTiles; d += kCols ? 1 : 2) {
+                    int part = (warp + turn) & 3;
+                    asm volatile("" : "+r"(part));   // else the branches become an index, and o goes to local memory
+                    if (part != d / (kTiles / 4)) continue;
 #pragma unroll
-                        for (int d = 0; d < HD / 8; ++d)
+                    for (int mt = 0; mt < kM; ++mt)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int h = e >> 1, r = 16 * mt + 8 * h + g;
-                                const int col = k8 ? 16 * (d >> 1) + 4 * t4 + 2 * (e & 1) + (d & 1)
-                                                   : 8 * d + 2 * t4 + (e & 1);
-                                const float x = o[mt][d][e] * f_row[mt][h];
-                                if (w == 0) meet.o[r][col] = x;
-                                else meet.o[r][col] += x;
+                        for (int h = 0; h < 2; ++h) {
+                            const float f = f_row[mt][h];
+                            if constexpr (kCols) {
+                                float2* at = reinterpret_cast<float2*>(&meet.o[2 * t4 + h][16 * d + 2 * g]);
+                                float2 v = make_float2(o[mt][d][h] * f, o[mt][d][2 + h] * f);
+                                if (turn) {
+                                    const float2 was = *at;
+                                    v.x += was.x;
+                                    v.y += was.y;
+                                }
+                                *at = v;
+                            } else {
+                                float4* at = reinterpret_cast<float4*>(&meet.o[16 * mt + 8 * h + g][8 * d + 4 * t4]);
+                                const float x0 = o[mt][d][2 * h] * f, x1 = o[mt][d][2 * h + 1] * f;
+                                const float y0 = o[mt][d + 1][2 * h] * f, y1 = o[mt][d + 1][2 * h + 1] * f;
+                                float4 v = k8 ? make_float4(x0, y0, x1, y1) : make_float4(x0, x1, y0, y1);
+                                if (turn) {
+                                    const float4 was = *at;
+                                    v.x += was.x;
+                                    v.y += was.y;
+                                    v.z += was.z;
+                                    v.w += was.w;
+                                }
+                                *at = v;
                             }
+                        }
                 }
                 __syncthreads();
             }
@@ -545,8 +751,22 @@ __global__ void __launch_bounds__(kThreads) k_paged_attn(const __grid_constant__
                 const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) sum += meet.l[w][r] * ex2(meet.m[w][r] - base);
-                const float4 x0 = *reinterpret_cast<const float4*>(&meet.o[r][8 * c]);
-                const float4 x1 = *reinterpret_cast<const float4*>(&meet.o[r][8 * c + 4]);
+                float4 x0, x1;
+                if constexpr (k8) {
+                    x0 = *reinterpret_cast<const float4*>(&meet.o[r][8 * c]);
+                    x1 = *reinterpret_cast<const float4*>(&meet.o[r][8 * c + 4]);
+                } else if constexpr (kCols) {
+                    const float* from = &meet.o[r][16 * (c >> 1) + (c & 1)];
+                    x0 = make_float4(from[0], from[2], from[4], from[6]);
+                    x1 = make_float4(from[8], from[10], from[12], from[14]);
+                } else {
+                    const float* from = &meet.o[r][16 * (c >> 1) + 2 * (c & 1)];
+                    float2 x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const float2*>(from + 4 * j);
+                    x0 = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+                    x1 = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+                }
                 if (whole) {
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
                     const int row = t.q.q0 + i / a.group, qh = t.head * a.group + i % a.group;
@@ -691,9 +911,9 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ JoinA
     }
 }
 
-// CTAs of the few-rows kernel: as many as stay resident (registers allow 3 an
-// SM with 16 rows and 2 with 32; shared memory may allow fewer).
-constexpr int kMaxCtasPerSm = 3;
+// CTAs of the few-rows kernel: as many as stay resident (ctas_of by the
+// registers; shared memory may allow fewer).
+constexpr int kMaxCtasPerSm = 4;
 
 template <int HD, Kind K, bool BF16, int MT>
 cudaError_t launch_few(AttnArgs& a, int* grid, int n_sm, cudaStream_t st) {
@@ -703,19 +923,20 @@ cudaError_t launch_few(AttnArgs& a, int* grid, int n_sm, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     const int by_smem = (int)(228 * 1024 / (smem + 1024));
-    *grid = n_sm * max(1, min(by_smem, MT == 1 ? kMaxCtasPerSm : 2));
+    *grid = n_sm * max(1, min(by_smem, ctas_of<MT>));
     // No more CTAs than the batch can have units.
     const long long tiles = ((long long)a.b.max_q * a.group + a.tile - 1) / a.tile;
     const long long units = (((long long)a.b.max_pages << a.kv.page_shift) + kUnit - 1) / kUnit;
     if (a.b.n_seq * tiles * a.kv.n_kv < *grid)
         *grid = (int)min((long long)*grid, a.b.n_seq * tiles * a.kv.n_kv * units);
-    a.parts = carve_parts(a.parts.info, *grid, 16 * MT);
+    a.parts = carve_parts(a.parts.info, *grid, rows_of<MT>);
     kern<<<*grid, kThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 template <int HD, Kind K, bool BF16>
 cudaError_t launch_rows(AttnArgs& a, int* grid, int n_sm, cudaStream_t st) {
+    if (a.tile == 8) return launch_few<HD, K, BF16, 0>(a, grid, n_sm, st);
     return a.tile == 16 ? launch_few<HD, K, BF16, 1>(a, grid, n_sm, st) : launch_few<HD, K, BF16, 2>(a, grid, n_sm, st);
 }
 
@@ -737,6 +958,7 @@ struct Plan {
 Plan plan_of(const Batch& b, const Pool& kv, int n_head, bool tensor) {
     const int group = n_head / kv.n_kv;
     const long long most = (long long)b.max_q * group;
+    if (most <= 8) return {8, 0x7fffffff, false};
     if (most <= 16) return {16, 0x7fffffff, false};
     if (most <= 32 || !tensor) return {32, 0x7fffffff, false};
     if (b.n_seq == 1) return {0, 0, true};
@@ -751,9 +973,10 @@ bool tensor_kernel(float scale) {
 
 long long attn_workspace(const Batch& b, const Pool& kv, int head_dim, int n_head, int n_sm) {
     const int group = n_head / kv.n_kv;
+    const long long most = (long long)b.max_q * group;
     // For either choice of kernels.
-    return parts_bytes(n_sm * kMaxCtasPerSm, (long long)b.max_q * group <= 16 ? 16 : 32, head_dim) +
-           ((long long)b.max_q * group > 32 ? parts_bytes(n_sm, tc_tile_rows(group), head_dim) : 0);
+    return parts_bytes(n_sm * kMaxCtasPerSm, most <= 8 ? 8 : most <= 16 ? 16 : 32, head_dim) +
+           (most > 32 ? parts_bytes(n_sm, tc_tile_rows(group), head_dim) : 0);
 }
 
 cudaError_t enqueue_attention(const Pool& kv, const Batch& b, const AttnCall& c, const Rows& q, const Rows& out,

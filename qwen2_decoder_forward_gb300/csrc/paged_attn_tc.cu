@@ -102,14 +102,13 @@ struct TcArgs {
     int sub_rows;         // R
     int k_stages, v_stages, raw_stages;
     int kv_rank[3];       // tensor-map dims (1..3) of position, head, page
-    int min_slots;
 };
 
 // The roles' loops together have to stay within the instruction cache (inlined
 // everywhere, the slow part of the waits and the walk over the work list made
 // instruction fetches the largest stall of the 8-bit kernels): those are calls.
-__device__ __noinline__ WorkList tc_build_work(const AttnArgs& a, long long* prefix, int min_slots) {
-    return build_work<kUnit, kCost>(a, prefix, min_slots);
+__device__ __noinline__ WorkList tc_build_work(const AttnArgs& a, long long* prefix) {
+    return build_work<kUnit, kCost, kCost + 4>(a, prefix);
 }
 __device__ __noinline__ Tile tc_find_tile(const AttnArgs& a, const WorkList& w) { return find_tile<kUnit, kCost>(a, w); }
 __device__ __noinline__ void tc_next_tile(const AttnArgs& a, const WorkList& w, Tile& t) {
@@ -441,7 +440,7 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    const WorkList work = tc_build_work(a, prefix, args.min_slots);
+    const WorkList work = tc_build_work(a, prefix);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1064,7 +1063,6 @@ cudaError_t enqueue_attention_tc(const TcMaps& m, const AttnArgs& a, int format,
     args.sub = a.tile / 2;
     args.sub_rows = args.sub / a.group;
     for (int i = 0; i < 3; ++i) args.kv_rank[i] = m.kv_rank[i];
-    args.min_slots = kCost + 4;
     if (format == QWEN2_KV_INT8) return launch_hd<kInt8>(m, args, head_dim, bf16, n_sm, chained, st);
     if (format == QWEN2_KV_E4M3) return launch_hd<kE4m3>(m, args, head_dim, bf16, n_sm, chained, st);
     return launch_hd<kSame16>(m, args, head_dim, bf16, n_sm, chained, st);
