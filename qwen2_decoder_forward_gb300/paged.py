@@ -187,6 +187,13 @@ class PagedBatch:
         self._at = ctypes.addressof(self._c)
         self._space = {}
 
+    def _with_rows(self, rows: int):
+        """The batch's descriptor for a call with ``rows`` rows: the call's own,
+        since calls from several threads may share the batch."""
+        c = _PagedBatch.from_buffer_copy(self._c)
+        c.n_rows = rows
+        return c
+
     def check(self):
         """Synchronises, and raises Qwen2Error (QWEN2_E_DEVICE_GUARD) if a
         value in the batch's tensors was bad in any call since the last check."""
@@ -289,8 +296,8 @@ def paged_write(kv: PagedKV, batch: PagedBatch, k, v, q=None, q_out=None, q_dtyp
             o.rope = _f32(rope, "rope", shape, dev)
             o.rope_rows, o.rotary_dim, o.interleaved = shape[0], 2 * shape[1], int(interleaved)
         po_opts = ctypes.addressof(o)
-    batch._c.n_rows = rows
-    rc = _lib().qwen2_paged_write(kv._at, batch._at, po_opts, n_head, pq, po, ctypes.addressof(rk), ctypes.addressof(rv),
+    b = batch._with_rows(rows)
+    rc = _lib().qwen2_paged_write(kv._at, ctypes.addressof(b), po_opts, n_head, pq, po, ctypes.addressof(rk), ctypes.addressof(rv),
                                   _raw_stream(kv._index))
     if rc:
         _check(rc)
@@ -344,7 +351,7 @@ def paged_attention(kv: PagedKV, batch: PagedBatch, q, out=None, scale=None, cau
         out = _t.empty(shape, dtype=q.dtype, device=dev)
     ro = _rows(out, "out", n_head, hd, rows, dev)
     lse = _t.empty((rows, n_head), dtype=_t.float32, device=dev) if return_lse else None
-    batch._c.n_rows = rows
+    b = batch._with_rows(rows)
     if workspace is None:
         key = (kv.n_kv_head, hd, n_head)
         need = batch._space.get(key)
@@ -355,7 +362,7 @@ def paged_attention(kv: PagedKV, batch: PagedBatch, q, out=None, scale=None, cau
         if workspace.dtype != _t.uint8 or workspace.device != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 tensor on the pool's device")
         need = workspace.numel()
-    rc = _lib().qwen2_paged_attention(kv._at, batch._at, n_head, ctypes.addressof(rq), ctypes.addressof(ro),
+    rc = _lib().qwen2_paged_attention(kv._at, ctypes.addressof(b), n_head, ctypes.addressof(rq), ctypes.addressof(ro),
                                       lse.data_ptr() if return_lse else None,
                                       hd ** -0.5 if scale is None else scale, int(causal), workspace.data_ptr(), need,
                                       _raw_stream(kv._index))
