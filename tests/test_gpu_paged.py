@@ -50,13 +50,13 @@ def coded(x, kind):
 class Case:
     """A batch of sequences given as (rows, cached positions) pairs."""
 
-    def __init__(self, q2, seqs, heads, fmt, page, layout="head", seed=0, spare_rows=3):
+    def __init__(self, q2, seqs, heads, fmt, page, layout="head", seed=0, spare_rows=3, before=0):
         self.q2, self.seqs, self.fmt, self.page = q2, seqs, fmt, page
         self.nh, self.nkv, self.hd = heads
         g = self.g = torch.Generator(device="cuda").manual_seed(seed)
         need = [-(-kv // page) for _, kv in seqs]
-        n_pages = sum(need) + 2
-        order = torch.randperm(n_pages, generator=g, device="cuda").to(torch.int32)
+        n_pages = before + sum(need) + 2      # `before`: pages in front that nothing uses
+        order = before + torch.randperm(n_pages - before, generator=g, device="cuda").to(torch.int32)
         self.width = max(need) + 1
         pages = torch.full((len(seqs), self.width), -7, dtype=torch.int32, device="cuda")   # unused entries: bad ids
         at = 0
@@ -325,6 +325,147 @@ def test_graph_replays_read_lengths_and_pages_anew(q2):
         graph.replay()
         captured = out.clone()
         assert torch.equal(captured, step())  # the same call outside the graph
+    c.batch.check()
+
+
+@pytest.mark.parametrize("fmt,dtype", [("f16", "f16"), ("bf16", "bf16"), ("int8", "bf16"), ("e4m3", "f16")])
+@pytest.mark.parametrize("n", [1, 2, 7, 8, 9, 16, 17, 31, 32, 33, 65, 127, 129])
+def test_row_counts_around_the_tiles(q2, n, fmt, dtype):
+    """As many packed rows as a tile has, one fewer and one more, for one query head a kv head."""
+    c = Case(q2, [(n, n), (n, 200), (max(n - 1, 0), 333), (1, 65)], (2, 2, 128), fmt, 64, seed=20 + n)
+    run_attention(c, dt(dtype))
+
+
+@pytest.mark.parametrize("heads", [(64, 1, 64), (64, 1, 128), (33, 3, 64), (80, 2, 64)])
+def test_wide_groups(q2, heads):
+    for fmt, dtype in (("f16", "f16"), ("int8", "bf16")):
+        run_attention(Case(q2, [(1, 100), (1, 700), (0, 3)], heads, fmt, 32, seed=21), dt(dtype))
+        run_attention(Case(q2, [(5, 70), (40, 40), (1, 9)], heads, fmt, 32, seed=22), dt(dtype))
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("fmt,dtype", [("f16", "f16"), ("int8", "f16"), ("e4m3", "bf16")])
+def test_page_sizes_of_both_kernels(q2, page, fmt, dtype):
+    for i, layout in enumerate(("head", "token", "padded")):
+        seqs = [(150, 700), (1, 257), (1, 256), (90, 90)]
+        run_attention(Case(q2, seqs, (14, 2, 64), fmt, page, layout, seed=23 + i), dt(dtype))
+        run_attention(Case(q2, [(1, 257), (1, 16), (1, 255)], (14, 2, 64), fmt, page, layout, seed=26 + i), dt(dtype))
+
+
+@pytest.mark.parametrize("n_seq", [31, 32, 33, 64, 65, 100, 1025, 4096])
+def test_many_sequences(q2, n_seq):
+    """Work lists of more sequences than a warp takes at a time; some hold no rows, and with `long` some have
+    several causal tiles."""
+    for long in (False, True):
+        lens = np.random.default_rng(n_seq).integers(1, 40, n_seq)
+        seqs = [(int(i % 5 != 3), int(x)) for i, x in enumerate(lens)]
+        if long:
+            for i in range(0, n_seq, 1 + n_seq // 7):
+                seqs[i] = (70 + i % 3 * 40, 150)
+        run_attention(Case(q2, seqs, (2, 1, 64), "f16", 16, seed=n_seq), torch.float16)
+
+
+def test_other_rows_that_are_not_finite(q2):
+    """NaN and infinite queries of one sequence and behind the last one reach no other sequence's rows."""
+    for seqs in ([(1, 90), (1, 200), (2, 64)], [(100, 400), (130, 130), (70, 300), (1, 90)]):
+        c = Case(q2, seqs, (14, 2, 64), "f16", 32, seed=28)
+        c.fill()
+        q = c.queries(torch.float16)
+        want = q2.paged_attention(c.kv, c.batch, q)[:c.live].clone()
+        q[c.starts[1]:c.starts[2]] = math.nan
+        q[c.starts[1]] = math.inf
+        q[c.live:] = math.nan
+        got = q2.paged_attention(c.kv, c.batch, q)[:c.live]
+        for s in range(len(seqs)):
+            if s != 1:
+                rows = slice(c.starts[s], c.starts[s + 1])
+                assert torch.equal(got[rows], want[rows])
+
+
+@pytest.mark.parametrize("n", [1, 3, 7, 200])
+def test_scales_that_grow_with_rows_of_every_tile(q2, n):
+    """v scales that double every 60 positions move G again and again, for each form of the row tiles."""
+    c = Case(q2, [(n, 900)], (8, 2, 128), "int8", 64, seed=29)
+    held = c.fill(0.0)
+    pos = torch.arange(900, device="cuda")
+    pg, off = c.pages[0][pos // 64].long(), pos % 64
+    sc = (2.0 ** (pos // 60).double() * 1e-3)[:, None].expand(900, c.nkv).float()
+    c.kv.v_scale[pg, :, off] = sc
+    codes = held[0][1][1]
+    held[0][1] = (codes * sc.double()[..., None], codes, sc.double()[..., None])
+    q = c.queries(torch.bfloat16)
+    out = torch.full_like(q, 7.0)
+    q2.paged_attention(c.kv, c.batch, q, out=out)
+    c.batch.check()
+    check_attention(c, q, held, out, None, c.hd ** -0.5, True, 7.0)
+
+
+@pytest.mark.parametrize("fmt,dtype", [("f16", "f16"), ("int8", "bf16")])
+def test_pages_beyond_four_gigabytes(q2, fmt, dtype):
+    """Every page in use lies more than 2^32 elements into the pool."""
+    before = (1 << 32) // (256 * 4 * 128) + 1
+    for seqs in ([(1, 700), (1, 30)], [(150, 600), (1, 40)]):
+        c = Case(q2, seqs, (8, 4, 128), fmt, 256, "token", seed=31, before=before)
+        run_attention(c, dt(dtype))
+        k, v = (c.normal(c.rows, 4, 128).to(dt(dtype)) for _ in range(2))
+        q2.paged_write(c.kv, c.batch, k, v)
+        n = sum(kv for _, kv in seqs)
+        starts = torch.tensor([0] + list(np.cumsum([kv for _, kv in seqs])), dtype=torch.int32, device="cuda")
+        gk, gv = q2.paged_read(c.kv, c.batch, starts, n)
+        c.batch.check()
+        for s, (rows, kv) in enumerate(seqs):
+            last = slice(int(starts[s]) + kv - rows, int(starts[s]) + kv)
+            for got, x in ((gk, k), (gv, v)):
+                x = x[c.starts[s]:c.starts[s] + rows].double()
+                # f16 holds it exactly; int8 is off by half a code and f32's roundings of scale and product.
+                off = 0 if fmt == "f16" else x.abs().amax(-1, keepdim=True) / 127 * (0.5 + 2.0 ** -15)
+                assert bool(((got[last].double() - x).abs() <= off).all())
+        del c, k, v, gk, gv
+        torch.cuda.empty_cache()
+
+
+def test_threads_and_graphs_at_the_same_time(q2):
+    """Two threads share a pool and a batch on streams of their own with different row buffers; two graphs of
+    the same call are replayed side by side."""
+    import threading
+    c = Case(q2, MIXES["chunks"] + MIXES["tokens"], (14, 2, 64), "int8", 32, seed=30)
+    c.fill()
+    q = c.queries(torch.float16)
+    qs = [q, torch.cat([q, q[:9]])]
+    want = [q2.paged_attention(c.kv, c.batch, x)[:c.live].clone() for x in qs]
+    assert torch.equal(want[0], want[1])
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(40):
+                o = q2.paged_attention(c.kv, c.batch, qs[i], stream=stream)
+                stream.synchronize()
+                if o.shape != qs[i].shape or not torch.equal(o[:c.live], want[0]):
+                    bad.append(i)
+        except Exception as e:      # noqa: BLE001
+            bad.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+    graphs, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(q2.paged_attention(c.kv, c.batch, q))
+        graphs.append(g)
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o[:c.live], want[0])
     c.batch.check()
 
 
