@@ -20,6 +20,11 @@ int refuse(int code, const std::string& msg) {
     set_thread_error(msg);
     return code;
 }
+// Who refuses what; put together only when a message needs it.
+struct Where {
+    const char *fn, *name;
+    std::string operator+(const char* msg) const { return std::string(fn) + (name ? std::string(": ") + name : "") + msg; }
+};
 
 bool mult16(long long bytes) { return bytes >= 0 && bytes % 16 == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -44,7 +49,7 @@ int guarded(const char* what, F f) {
 constexpr long long kMaxStride = 1ll << 40;   // elements; keeps every offset inside 64 bits
 
 int check_pool(const char* fn, const qwen2_paged_kv* c, Pool& p) {
-    const std::string at(fn);
+    const Where at{fn, nullptr};
     if (!c) return refuse(QWEN2_E_ARG, at + ": kv is NULL");
     if (c->format < QWEN2_KV_F16 || c->format > QWEN2_KV_E4M3)
         return refuse(QWEN2_E_UNSUPPORTED, at + ": page format " + std::to_string(c->format) + " is not supported");
@@ -79,7 +84,7 @@ int check_pool(const char* fn, const qwen2_paged_kv* c, Pool& p) {
 }
 
 int check_batch(const char* fn, const qwen2_paged_batch* c, int page_size, bool rows, Batch& b) {
-    const std::string at(fn);
+    const Where at{fn, nullptr};
     if (!c) return refuse(QWEN2_E_ARG, at + ": batch is NULL");
     if (c->n_seq < 1 || c->n_seq > 4096) return refuse(QWEN2_E_ARG, at + ": n_seq outside [1, 4096]");
     if (!c->kv_len || !c->pages || (rows && !c->q_start)) return refuse(QWEN2_E_ARG, at + ": null batch array");
@@ -102,7 +107,7 @@ int check_batch(const char* fn, const qwen2_paged_batch* c, int page_size, bool 
 }
 
 int check_rows(const char* fn, const char* name, const qwen2_rows* r, Rows& o) {
-    const std::string at = std::string(fn) + ": " + name;
+    const Where at{fn, name};
     if (!r || !r->data) return refuse(QWEN2_E_ARG, at + " is NULL");
     if (r->dtype < QWEN2_DTYPE_F32 || r->dtype > QWEN2_DTYPE_BF16)
         return refuse(QWEN2_E_UNSUPPORTED, at + " has an unknown dtype");

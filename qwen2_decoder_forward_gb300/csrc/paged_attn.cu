@@ -8,17 +8,32 @@
 // row (online softmax).  Bound by HBM: every cached byte is read once, for
 // group * rows products of 2 hd flops, far below the tensor cores' rate.
 //
-// Split (paged.cuh): a tile is up to kRows = 16 MT packed rows of one kv head,
+// Split (paged.cuh): a tile is up to 8, 16 or 32 packed rows of one kv head,
 // a unit 64 positions.  Inside a CTA warp w takes positions 16 w .. 16 w + 15
 // of every unit on its own: its loads, softmax statistics and accumulators
 // are the warp's, so the main loop has no block barrier.  The four warps meet
 // at a tile's end in shared memory.  16 positions never cross a page, so a
-// step needs one page lookup, loaded a step before its copies are issued.
+// step needs one page lookup, loaded a step before its copies are issued (the
+// first steps' all at once, a lane each).
 //
 // Loads: cp.async in 16-byte pieces, kStages steps in flight per warp, and
 // positions past the tile's keys are filled with zeros instead of read (what
-// a page holds there may be NaN).  Products: mma m16n8k16, the rows in M and
-// the positions (scores) or dims (values) in N.
+// a page holds there may be NaN).  Products: mma m16n8k16.  16 or 32 rows
+// stand in M, positions (scores) or dims (values) in N.  Up to 8 rows, the
+// single token of 8 or fewer query heads a kv head, stand in N, positions or
+// dims in M: half the products, half the softmax and half the accumulators of
+// a 16-row tile half empty, and the probabilities only need an 8 x 8
+// transpose on their way into the second product.
+//
+// Measured (16 tokens over 8,000 - 32,700 positions of int8, 28 heads on 4,
+// 346 MB): 73 us, 4.7 TB/s.  Instructions bound it, about 420 a step of 16
+// positions and warp, 64% of the issue slots with four CTAs an SM: two thirds
+// of them widen codes and issue copies.  With the rows in M it took 88 us with
+// three CTAs an SM and 115 us with two (the registers of 64 accumulators more,
+// and a ring of four stages).  One token over 999 positions takes 7.6 us, of
+// which the join and the two launches' latencies are some 4; the rest is a
+// chain of a few load latencies (lengths, page ids, pages) per CTA, and so it
+// is for 32 tokens over 256 - 4,095 of f16: 16.1 us for 36 MB.
 //
 // 8-bit pages: codes become exact f16 in registers (int8: 1024 + (c + 128)
 // by a byte permute, minus 1152; e4m3: the hardware conversion) and the f32

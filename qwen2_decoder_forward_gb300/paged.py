@@ -10,11 +10,12 @@ Argument marshalling only; every check that needs a value in device memory is
 the kernels' own and is reported through ``PagedBatch.check``.  Calls do not
 synchronise and may be captured into a CUDA graph: a replay reads the batch's
 tensors anew.  Outputs and workspaces come from torch's allocator on the
-stream of the call.
+stream of the call; threads may share a pool and a batch.
 """
 from __future__ import annotations
 
 import ctypes
+from threading import get_ident as _thread
 
 import numpy as np
 
@@ -87,7 +88,7 @@ _t = None        # torch, once it is needed
 
 
 def _types():
-    global _t, _raw_stream
+    global _t, _raw_stream, _capturing
     if _t is None:
         import torch
         _formats.update({torch.float16: KV_F16, torch.bfloat16: KV_BF16, torch.int8: KV_INT8,
@@ -96,6 +97,7 @@ def _types():
         # The current stream's pointer, without building a Stream object for it.
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _capturing = torch.cuda.is_current_stream_capturing
         _t = torch
     return _t
 
@@ -185,7 +187,8 @@ class PagedBatch:
         self._c = _PagedBatch(n, 0, self.max_q, pages.shape[1], stride, q_start.data_ptr(), kv_len.data_ptr(),
                               pages.data_ptr(), self.guard.data_ptr())
         self._at = ctypes.addressof(self._c)
-        self._space = {}
+        self._space = {}      # workspace bytes by shapes
+        self._buffers = {}    # workspaces by stream and thread
 
     def _with_rows(self, rows: int):
         """The batch's descriptor for a call with ``rows`` rows: the call's own,
@@ -331,6 +334,24 @@ def paged_read(kv: PagedKV, batch: PagedBatch, out_start, n_rows: int, dtype=Non
     return k_out, v_out
 
 
+def _workspace(kv, batch, n_head, stream):
+    """The batch's workspace on a stream, where one thread's calls come one after
+    another (two threads' launches may alternate there, so each has its own); a
+    call that is captured gets a new one, since its graph may be replayed beside
+    anything."""
+    key = (kv.n_kv_head, kv.head_dim, n_head)
+    need = batch._space.get(key)
+    if need is None:
+        need = batch._space[key] = paged_attention_workspace(kv, batch, n_head)
+    if _capturing():
+        return _t.empty(need, dtype=_t.uint8, device=kv.device), need
+    at = (stream, _thread())
+    w = batch._buffers.get(at)
+    if w is None or w.numel() < need:
+        w = batch._buffers[at] = _t.empty(need, dtype=_t.uint8, device=kv.device)
+    return w, need
+
+
 def paged_attention(kv: PagedKV, batch: PagedBatch, q, out=None, scale=None, causal: bool = True,
                     return_lse: bool = False, workspace=None, stream=None):
     """Attention of the batch's rows ``q`` ([rows, n_head, head_dim], f16 or
@@ -339,7 +360,8 @@ def paged_attention(kv: PagedKV, batch: PagedBatch, q, out=None, scale=None, cau
     of them.  Returns o like q, with ``return_lse`` also f32 [rows, n_head]:
     the log of the sum of exp(scale q.k), -inf for a row without keys (whose o
     is 0).  ``scale``: default head_dim^-1/2.  ``workspace``: a uint8 CUDA
-    tensor of ``paged_attention_workspace`` bytes (default: allocated here)."""
+    tensor of ``paged_attention_workspace`` bytes (default: the batch keeps one
+    for each stream and thread that use it; a captured call has its own)."""
     if not _plain(kv, batch, stream):
         with _Call(kv, batch, stream):
             return paged_attention(kv, batch, q, out, scale, causal, return_lse, workspace)
@@ -348,24 +370,20 @@ def paged_attention(kv: PagedKV, batch: PagedBatch, q, out=None, scale=None, cau
     shape = q.shape
     rows, n_head = shape[0], shape[1]
     if out is None:
-        out = _t.empty(shape, dtype=q.dtype, device=dev)
+        out = _t.empty_like(q)
     ro = _rows(out, "out", n_head, hd, rows, dev)
     lse = _t.empty((rows, n_head), dtype=_t.float32, device=dev) if return_lse else None
     b = batch._with_rows(rows)
+    stream = _raw_stream(kv._index)
     if workspace is None:
-        key = (kv.n_kv_head, hd, n_head)
-        need = batch._space.get(key)
-        if need is None:
-            need = batch._space[key] = paged_attention_workspace(kv, batch, n_head)
-        workspace = _t.empty(need, dtype=_t.uint8, device=dev)
+        workspace, need = _workspace(kv, batch, n_head, stream)
     else:
         if workspace.dtype != _t.uint8 or workspace.device != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 tensor on the pool's device")
         need = workspace.numel()
     rc = _lib().qwen2_paged_attention(kv._at, ctypes.addressof(b), n_head, ctypes.addressof(rq), ctypes.addressof(ro),
                                       lse.data_ptr() if return_lse else None,
-                                      hd ** -0.5 if scale is None else scale, int(causal), workspace.data_ptr(), need,
-                                      _raw_stream(kv._index))
+                                      hd ** -0.5 if scale is None else scale, int(causal), workspace.data_ptr(), need, stream)
     if rc:
         _check(rc)
     return (out, lse) if return_lse else out

@@ -437,22 +437,23 @@ def test_threads_and_graphs_at_the_same_time(q2):
     torch.cuda.synchronize()
     bad = []
 
-    def work(i):
+    def work(i, own):
         try:
-            stream = torch.cuda.Stream()
+            stream = torch.cuda.Stream() if own else None
             for _ in range(40):
                 o = q2.paged_attention(c.kv, c.batch, qs[i], stream=stream)
-                stream.synchronize()
+                (stream or torch.cuda.current_stream()).synchronize()
                 if o.shape != qs[i].shape or not torch.equal(o[:c.live], want[0]):
                     bad.append(i)
         except Exception as e:      # noqa: BLE001
             bad.append(e)
-    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
-    for t in threads:
-        t.start()
-    for t in threads:
-        t.join()
-    assert not bad
+    for own in (True, False):       # streams of their own, then one stream
+        threads = [threading.Thread(target=work, args=(i, own)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not bad
     graphs, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
     for i in range(2):
         g = torch.cuda.CUDAGraph()
