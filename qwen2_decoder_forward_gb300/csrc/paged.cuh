@@ -90,20 +90,22 @@ struct PartInfo {
 struct Parts {
     PartInfo* info;   // [g]
     float* ml;        // [2 g][2][rows]: row maxima (base 2), sums
-    float* o;         // [2 g][rows][hd]
+    float* o;         // [2 g][rows][hd], or (beside) [2 g][hd / 4][rows][4]
     int rows;
+    bool beside;      // rows side by side, four dims each
 };
 __host__ __device__ inline long long parts_bytes(int g, int rows, int hd) {
     const long long b = (long long)g * (sizeof(PartInfo) + 2 * (2ll * rows * 4 + (long long)rows * hd * 4));
     return (b + 255) / 256 * 256;
 }
-inline Parts carve_parts(void* ws, int g, int rows) {
+inline Parts carve_parts(void* ws, int g, int rows, bool beside) {
     Parts p;
     char* c = static_cast<char*>(ws);
     p.info = reinterpret_cast<PartInfo*>(c);
     p.ml = reinterpret_cast<float*>(c + (long long)g * sizeof(PartInfo));
     p.o = p.ml + 4ll * g * rows;
     p.rows = rows;
+    p.beside = beside;
     return p;
 }
 

@@ -26,9 +26,9 @@
 // transpose on their way into the second product.
 //
 // Measured (16 tokens over 8,000 - 32,700 positions of int8, 28 heads on 4,
-// 346 MB): 73 us, 4.7 TB/s.  Instructions bound it, about 420 a step of 16
-// positions and warp, 64% of the issue slots with four CTAs an SM: two thirds
-// of them widen codes and issue copies.  With the rows in M it took 88 us with
+// 346 MB): 73 us, 4.7 TB/s.  Instructions bound it, about 580 a step of 16
+// positions and warp (a third of them widens the codes), which fill 64% of the
+// issue slots with four CTAs an SM.  With the rows in M it took 88 us with
 // three CTAs an SM and 115 us with two (the registers of 64 accumulators more,
 // and a ring of four stages).  One token over 999 positions takes 7.6 us, of
 // which the join and the two launches' latencies are some 4; the rest is a
@@ -841,8 +841,12 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ JoinA
     const Parts& parts = a.parts[which];
     const PartInfo info = parts.info[c0];
     if (info.n == 0) return;
-    const int g = threadIdx.x / kT, d = threadIdx.x % kT;
+    // Neighbouring threads take neighbouring dims or rows, as the partials lie.
+    const int g = parts.beside ? threadIdx.x % kGroups : threadIdx.x / kT;
+    const int d = parts.beside ? threadIdx.x / kGroups : threadIdx.x % kT;
+    const int g_step = parts.beside ? 1 : kT;              // threads from a group to the next
     const int rows = parts.rows, n = min(info.n, a.n_cta[which] - c0);
+    const int d_step = parts.beside ? rows : 1, r_step = parts.beside ? 1 : kT;
     const int share = n > kAhead ? 4 : 1;                  // groups per row
     const int sub = g % share;
     const int at_once = kGroups / share;
@@ -866,7 +870,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ JoinA
                         const long long slot = k == 0 ? 2 * c0 + 1 : 2 * (c0 + k);
                         m[i] = parts.ml[slot * 2 * rows + r];
                         l[i] = parts.ml[(slot * 2 + 1) * rows + r];
-                        o[i] = reinterpret_cast<const float4*>(parts.o + (slot * rows + r) * HD)[d];
+                        o[i] = reinterpret_cast<const float4*>(parts.o + slot * rows * HD)[d * d_step + r * r_step];
                     }
                 }
                 float t = top;
@@ -906,7 +910,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ JoinA
             acc = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int i = 0; i < share; ++i) {
                 const float w = ex2(sm_[first + i] - base);
-                const float4 o = so[(first + i) * kT + d];
+                const float4 o = so[threadIdx.x + (i - sub) * g_step];
                 sum = fmaf(sl[first + i], w, sum);
                 acc.x = fmaf(o.x, w, acc.x);
                 acc.y = fmaf(o.y, w, acc.y);
@@ -944,7 +948,7 @@ cudaError_t launch_few(AttnArgs& a, int* grid, int n_sm, cudaStream_t st) {
     const long long units = (((long long)a.b.max_pages << a.kv.page_shift) + kUnit - 1) / kUnit;
     if (a.b.n_seq * tiles * a.kv.n_kv < *grid)
         *grid = (int)min((long long)*grid, a.b.n_seq * tiles * a.kv.n_kv * units);
-    a.parts = carve_parts(a.parts.info, *grid, rows_of<MT>);
+    a.parts = carve_parts(a.parts.info, *grid, rows_of<MT>, false);
     kern<<<*grid, kThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
@@ -1033,7 +1037,7 @@ cudaError_t enqueue_attention(const Pool& kv, const Batch& b, const AttnCall& c,
         a.tile = tc_tile_rows(a.group);
         a.rows_lo = plan.tile ? plan.few : 0;
         a.rows_hi = 0x7fffffff;
-        a.parts = carve_parts(ws, n_sm, a.tile);
+        a.parts = carve_parts(ws, n_sm, a.tile, true);
         e = enqueue_attention_tc(maps, a, c.format, c.head_dim, bf16, n_sm, plan.tile != 0, st);
         if (e != cudaSuccess) return e;
         j.parts[1] = a.parts;

@@ -42,8 +42,8 @@
 // v's the probabilities, relative to G, the largest v scale so far rounded up
 // to a power of two, which O carries like the reference m.
 //
-// Measured: a prompt of 5,001 rows (28 heads on 4 of 128, bf16) 208 us, 865
-// TFLOP/s; 1,024 rows after 31,000 positions of e4m3 614 us, 753 TFLOP/s.  A
+// Measured: a prompt of 5,001 rows (28 heads on 4 of 128, bf16) 203 us, 883
+// TFLOP/s; 1,024 rows after 31,000 positions of e4m3 606 us, 763 TFLOP/s.  A
 // unit takes some 1,930 cycles, of which the products are about 1,950 for
 // both halves (16 of S at 79 cycles each, 8 of P V at 86): the tensor pipe is
 // what bounds it, at half its rate in S, since an M = 128 product of N = 64
@@ -117,10 +117,16 @@ struct TcArgs {
 // The roles' loops together have to stay within the instruction cache (inlined
 // everywhere, the slow part of the waits and the walk over the work list made
 // instruction fetches the largest stall of the 8-bit kernels): those are calls.
-__device__ __noinline__ WorkList tc_build_work(const AttnArgs& a, long long* prefix) {
-    return build_work<kUnit, kCost, kCost + 4>(a, prefix);
-}
+// The 8-bit kernels, with one role more, call for their first tile as well:
+// 1,024 rows after 31,000 positions of e4m3 take 606 us so and 661 us without;
+// the others are quicker on their way to it without the call (a call reads the
+// kernel's parameters from memory): a batch of short chunks 31.5 against 32.7 us.
 __device__ __noinline__ Tile tc_find_tile(const AttnArgs& a, const WorkList& w) { return find_tile<kUnit, kCost>(a, w); }
+template <bool kCall>
+__device__ __forceinline__ Tile first_tile(const AttnArgs& a, const WorkList& w) {
+    if constexpr (kCall) return tc_find_tile(a, w);
+    else return find_tile<kUnit, kCost>(a, w);
+}
 __device__ __noinline__ void tc_next_tile(const AttnArgs& a, const WorkList& w, Tile& t) {
     next_tile<kUnit, kCost>(a, w, t);
 }
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     pdl_launch_dependents();
-    if (tid == 0) {
+    if (tid == 9 * 32) {
 #pragma unroll 1
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sm.k_full[i], k8 ? kFeeders : 1);
@@ -450,14 +456,14 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
     }
-    const WorkList work = tc_build_work(a, prefix);
+    const WorkList work = build_work<kUnit, kCost, kCost + 4>(a, prefix);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_slot;
     bool open = false;
     if (work.begin < work.end) {
-        Tile t = tc_find_tile(a, work);
+        Tile t = first_tile<k8>(a, work);
         if (warp < 8) {
             // ---- softmax of half x --------------------------------------------------
             const int x = warp >> 2, rl = 32 * (warp & 3) + lane;
@@ -601,26 +607,28 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                     const float l = l0 + l1, unit_g = k8 ? pow2i(g) : 1.f;
                     const PartPlace place = part_place(t);
                     const int r = x * args.sub + rl;
-                    // Rows go out through the warp's staging buffer: 64 bytes of each of its 32 rows
+                    // Finished rows go out through the warp's staging buffer: 64 bytes of each of its 32 rows
                     // at a time, written a row per lane and stored four lanes a row (a row per lane
                     // straight to memory touches 32 lines a store and holds the load / store unit
-                    // for 5,000 cycles a tile).
+                    // for 5,000 cycles a tile).  Partials keep four dims of all rows side by side
+                    // instead, so that a row per lane is a line (7,500 cycles a tile through the
+                    // staging buffer).
                     const float f = !place.whole ? unit_g : l == 0.f ? 0.f : unit_g / l;
-                    char* dst;
+                    char* dst = nullptr;
+                    float4* part = nullptr;
                     if (place.whole) {
                         const int row = t.q.q0 + i / a.group, qh = t.head * a.group + i % a.group;
-                        dst = a.out.data + (long long)row * a.out.row_bytes + (long long)qh * a.out.head_bytes;
+                        if (live) dst = a.out.data + (long long)row * a.out.row_bytes + (long long)qh * a.out.head_bytes;
                         if (live && a.lse)
                             a.lse[(long long)row * a.n_head + qh] =
                                 l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
                     } else {
-                        dst = reinterpret_cast<char*>(a.parts.o + ((long long)place.slot * a.parts.rows + r) * HD);
+                        part = reinterpret_cast<float4*>(a.parts.o + (long long)place.slot * a.parts.rows * HD) + r;
                         if (live) {
                             a.parts.ml[(long long)place.slot * 2 * a.parts.rows + r] = m;
                             a.parts.ml[((long long)place.slot * 2 + 1) * a.parts.rows + r] = l;
                         }
                     }
-                    if (!live) dst = nullptr;
                     const uint32_t stage = staging + 2048 * warp;
 #pragma unroll 1
                     for (int c = 0; c < HD / 32; ++c) {
@@ -636,9 +644,11 @@ __global__ void __launch_bounds__(kThreadsOf<K>, 1)
                             put_rows64(stage, w, dst, 64 * c, lane);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            put_rows64(stage, reinterpret_cast<const uint32_t(&)[16]>(o[0]), dst, 128 * c, lane);
-                            put_rows64(stage, reinterpret_cast<const uint32_t(&)[16]>(o[16]), dst, 128 * c + 64, lane);
+                            for (int e = 0; e < 8; ++e)
+                                if (live)
+                                    part[(long long)(8 * c + e) * a.parts.rows] = make_float4(
+                                        __uint_as_float(o[4 * e]) * f, __uint_as_float(o[4 * e + 1]) * f,
+                                        __uint_as_float(o[4 * e + 2]) * f, __uint_as_float(o[4 * e + 3]) * f);
                         }
                     }
                     if (!place.whole && place.begins) {
