@@ -822,36 +822,119 @@ struct JoinArgs {
 };
 
 // Adds up the tile that a CTA left open: its slot 1 and the slots 0 of the
-// CTAs after it.  blockIdx.x counts the CTAs of the first kernel, then those
-// of the second.  HD / 4 threads take a row, four dims each; with many parts
-// (a long sequence alone) four such groups share a row's parts.  The kernel is
-// a chain of latencies (which tile, its maxima, its rows): every load of a
-// step is issued before the first is used, and the grid is small, since most
-// CTAs left nothing open (7,296 blocks that only look cost 6 us, 912 less
-// than 2).
-template <int HD, bool BF16>
+// CTAs after it.  kFewShare blocks share the tile of a CTA of the few-rows
+// kernel, kTcShare that of one of the tensor-core kernel (up to 256 rows: a
+// tile in up to four parts is one round of loads).  HD / 4 threads take a row,
+// four dims each; with many parts (a long sequence alone) four such groups
+// share a row's parts.  The kernel is a chain of latencies (which tile, its
+// maxima, its rows): every load of a step is issued before the first is used,
+// and the grid is small, since most CTAs left nothing open (7,296 blocks that
+// only look cost 6 us, 912 less than 2).
+constexpr int kFewShare = 2, kTcShare = 16;
+
+// One joined row's four dims, and by the first of its threads the row's lse.
+template <bool BF16>
+__device__ __forceinline__ void put_joined(const JoinArgs& a, const PartInfo& info, int r, int d, float4 acc, float top,
+                                           float sum) {
+    const int i = info.packed0 + r;
+    const int row = info.q0 + i / a.group, qh = info.head * a.group + i % a.group;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2*>(a.out.data + (long long)row * a.out.row_bytes + (long long)qh * a.out.head_bytes + 8 * d) =
+        make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+    if (a.lse && d == 0)
+        a.lse[(long long)row * a.n_head + qh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// The rows first, first + step, ... of a tile cut in n <= P parts, R of them at a time.
+template <int HD, bool BF16, int P, int R>
+__device__ __forceinline__ void join_rows(const JoinArgs& a, const Parts& parts, const PartInfo& info, int c0, int n,
+                                          int first, int step, int d, int d_step, int r_step) {
+    const int rows = parts.rows, live = info.packed_end - info.packed0;
+    for (int r0 = first; r0 < live; r0 += R * step) {
+        float m[R][P], l[R][P];
+        float4 o[R][P];
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                const int r = r0 + j * step;
+                m[j][k] = -INFINITY;
+                l[j][k] = 0.f;
+                o[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < live && k < n) {
+                    const long long slot = k == 0 ? 2 * c0 + 1 : 2 * (c0 + k);
+                    m[j][k] = parts.ml[slot * 2 * rows + r];
+                    l[j][k] = parts.ml[(slot * 2 + 1) * rows + r];
+                    o[j][k] = reinterpret_cast<const float4*>(parts.o + slot * rows * HD)[d * d_step + r * r_step];
+                }
+            }
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const int r = r0 + j * step;
+            if (r >= live) break;
+            float top = m[j][0];
+#pragma unroll
+            for (int k = 1; k < P; ++k) top = fmaxf(top, m[j][k]);
+            const float base = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                const float w = ex2(m[j][k] - base);
+                sum = fmaf(l[j][k], w, sum);
+                acc.x = fmaf(o[j][k].x, w, acc.x);
+                acc.y = fmaf(o[j][k].y, w, acc.y);
+                acc.z = fmaf(o[j][k].z, w, acc.z);
+                acc.w = fmaf(o[j][k].w, w, acc.w);
+            }
+            put_joined<BF16>(a, info, r, d, acc, top, sum);
+        }
+    }
+}
+
+// kTc: the tensor-core kernel ran too (the few-rows kernel's tiles alone do not
+// need the code for its larger ones: half a microsecond of instruction fetches).
+template <int HD, bool BF16, bool kTc>
 __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ JoinArgs a) {
     constexpr int kT = HD / 4, kGroups = 256 / kT, kAhead = 8;
     __shared__ float4 so[256];
     __shared__ float sm_[kGroups], sl[kGroups];
     pdl_launch_dependents();
     pdl_wait();
-    const int which = (int)blockIdx.x >= a.n_cta[0];
-    const int c0 = blockIdx.x - (which ? a.n_cta[0] : 0);
+    int which = 0, c0 = blockIdx.x, y = blockIdx.y, ny = kFewShare;
+    if constexpr (kTc) {
+        const int few_blocks = kFewShare * a.n_cta[0];
+        which = (int)blockIdx.x >= few_blocks;
+        ny = which ? kTcShare : kFewShare;
+        const int at = blockIdx.x - (which ? few_blocks : 0);
+        c0 = at / ny;
+        y = at % ny;
+    }
     const Parts& parts = a.parts[which];
     const PartInfo info = parts.info[c0];
     if (info.n == 0) return;
     // Neighbouring threads take neighbouring dims or rows, as the partials lie.
-    const int g = parts.beside ? threadIdx.x % kGroups : threadIdx.x / kT;
-    const int d = parts.beside ? threadIdx.x / kGroups : threadIdx.x % kT;
-    const int g_step = parts.beside ? 1 : kT;              // threads from a group to the next
+    const int g = kTc && parts.beside ? threadIdx.x % kGroups : threadIdx.x / kT;
+    const int d = kTc && parts.beside ? threadIdx.x / kGroups : threadIdx.x % kT;
+    const int g_step = kTc && parts.beside ? 1 : kT;              // threads from a group to the next
     const int rows = parts.rows, n = min(info.n, a.n_cta[which] - c0);
-    const int d_step = parts.beside ? rows : 1, r_step = parts.beside ? 1 : kT;
+    const int d_step = kTc && parts.beside ? rows : 1, r_step = kTc && parts.beside ? 1 : kT;
+    if constexpr (kTc) {
+        // Tiles cut in a few parts: the loads of several rows at a time.
+        if (n <= 2) {
+            // Half the blocks do: with all of them a prompt's join took 20 us instead of 15.
+            if (y < ny / 2)
+                join_rows<HD, BF16, 2, 4>(a, parts, info, c0, n, kGroups * y + g, kGroups * (ny / 2), d, d_step, r_step);
+            return;
+        }
+        if (n <= 4)
+            return join_rows<HD, BF16, 4, 2>(a, parts, info, c0, n, kGroups * y + g, kGroups * ny, d, d_step, r_step);
+    }
     const int share = n > kAhead ? 4 : 1;                  // groups per row
     const int sub = g % share;
     const int at_once = kGroups / share;
     // Every thread takes every turn (the barriers below).
-    for (int r0 = blockIdx.y * at_once; info.packed0 + r0 < info.packed_end; r0 += gridDim.y * at_once) {
+    for (int r0 = y * at_once; info.packed0 + r0 < info.packed_end; r0 += ny * at_once) {
         const int r = r0 + g / share;
         const bool in = info.packed0 + r < info.packed_end;
         float top = -INFINITY, sum = 0.f;
@@ -920,13 +1003,7 @@ __global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ JoinA
             __syncthreads();
         }
         if (!in || sub) continue;
-        const int i = info.packed0 + r;
-        const int row = info.q0 + i / a.group, qh = info.head * a.group + i % a.group;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2*>(a.out.data + (long long)row * a.out.row_bytes + (long long)qh * a.out.head_bytes + 8 * d) =
-            make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
-        if (a.lse && d == 0)
-            a.lse[(long long)row * a.n_head + qh] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        put_joined<BF16>(a, info, r, d, acc, top, sum);
     }
 }
 
@@ -964,6 +1041,17 @@ cudaError_t launch_kind(AttnArgs& a, int format, int* grid, int n_sm, cudaStream
     if (format == QWEN2_KV_INT8) return launch_rows<HD, kInt8, BF16>(a, grid, n_sm, st);
     if (format == QWEN2_KV_E4M3) return launch_rows<HD, kE4m3, BF16>(a, grid, n_sm, st);
     return launch_rows<HD, kSame16, BF16>(a, grid, n_sm, st);
+}
+
+template <int HD>
+cudaError_t launch_join(const JoinArgs& j, bool bf16, bool tc, cudaStream_t st) {
+    const dim3 block(256);
+    const dim3 grid = tc ? dim3(kFewShare * j.n_cta[0] + kTcShare * j.n_cta[1]) : dim3(j.n_cta[0], kFewShare);
+    if (tc)
+        return bf16 ? launch_pdl(k_attn_join<HD, true, true>, grid, block, 0, st, j)
+                    : launch_pdl(k_attn_join<HD, false, true>, grid, block, 0, st, j);
+    return bf16 ? launch_pdl(k_attn_join<HD, true, false>, grid, block, 0, st, j)
+                : launch_pdl(k_attn_join<HD, false, false>, grid, block, 0, st, j);
 }
 
 // Which kernels a call needs.  Sequences of up to 32 packed rows are the
@@ -1043,12 +1131,7 @@ cudaError_t enqueue_attention(const Pool& kv, const Batch& b, const AttnCall& c,
         j.parts[1] = a.parts;
         j.n_cta[1] = n_sm;
     }
-    const dim3 grid(j.n_cta[0] + j.n_cta[1], plan.tc ? 8 : 2), block(256);
-    if (c.head_dim == 64)
-        return bf16 ? launch_pdl(k_attn_join<64, true>, grid, block, 0, st, j)
-                    : launch_pdl(k_attn_join<64, false>, grid, block, 0, st, j);
-    return bf16 ? launch_pdl(k_attn_join<128, true>, grid, block, 0, st, j)
-                : launch_pdl(k_attn_join<128, false>, grid, block, 0, st, j);
+    return c.head_dim == 64 ? launch_join<64>(j, bf16, plan.tc, st) : launch_join<128>(j, bf16, plan.tc, st);
 }
 
 }  // namespace paged
