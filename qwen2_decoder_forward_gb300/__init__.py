@@ -408,13 +408,15 @@ class Qwen2Model:
         """Copy positions 0..n-1 of one sequence's cache into paged pools
         (``pools``: one PagedKV per layer; ``pages``: int32 CUDA tensor, the
         page ids of the sequence in every pool), in the pools' format.  The
-        call is ordered on the stream like any other."""
-        self._page_rows(seq_id, n, pools, pages, stream, save=True)
+        call is ordered on the stream like any other; ``check()`` of the
+        PagedBatch it returns reports page ids outside the pools."""
+        return self._page_rows(seq_id, n, pools, pages, stream, save=True)
 
     def load_pages(self, seq_id: int, n: int, pools, pages, stream=None):
         """Bring positions 0..n-1 that save_pages stored back into a sequence
-        slot of the cache (any slot, any model of the same shape)."""
-        self._page_rows(seq_id, n, pools, pages, stream, save=False)
+        slot of the cache (any slot, any model of the same shape).  Returns a
+        PagedBatch to ``check()``, as save_pages does."""
+        return self._page_rows(seq_id, n, pools, pages, stream, save=False)
 
     def _page_rows(self, seq_id, n, pools, pages, stream, save):
         import torch
@@ -438,6 +440,7 @@ class Qwen2Model:
                     paged_write(pool, batch, k, v)
                 else:
                     paged_read(pool, batch, ends, n, k_out=k, v_out=v)
+        return batch
 
     def test_raise_guard(self, code: int, stream=None):
         """Test hook: write ``code`` into the device guard word (as a kernel's

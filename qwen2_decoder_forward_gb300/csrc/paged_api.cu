@@ -304,7 +304,7 @@ int qwen2_paged_attention(const qwen2_paged_kv* kv, const qwen2_paged_batch* bat
             (kv->format == QWEN2_KV_BF16 && q->dtype != QWEN2_DTYPE_BF16))
             return refuse(QWEN2_E_UNSUPPORTED, "qwen2_paged_attention: 16-bit pages need queries of their own type");
         if (!std::isfinite(scale)) return refuse(QWEN2_E_ARG, "qwen2_paged_attention: scale must be finite");
-        if (b.n_rows == 0 || b.max_q == 0) return QWEN2_OK;
+        if (b.n_rows == 0) return QWEN2_OK;
         int n_sm = 0;
         if ((r = sm_count(&n_sm)) != QWEN2_OK) return r;
         const int64_t need = attn_workspace(b, p, kv->head_dim, n_head, n_sm);

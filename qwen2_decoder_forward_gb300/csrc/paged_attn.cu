@@ -1020,11 +1020,11 @@ cudaError_t launch_few(AttnArgs& a, int* grid, int n_sm, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const int by_smem = (int)(228 * 1024 / (smem + 1024));
     *grid = n_sm * max(1, min(by_smem, ctas_of<MT>));
-    // No more CTAs than the batch can have units.
+    // No more CTAs than the batch can have units (one, which looks the batch over, if max_q is 0).
     const long long tiles = ((long long)a.b.max_q * a.group + a.tile - 1) / a.tile;
     const long long units = (((long long)a.b.max_pages << a.kv.page_shift) + kUnit - 1) / kUnit;
     if (a.b.n_seq * tiles * a.kv.n_kv < *grid)
-        *grid = (int)min((long long)*grid, a.b.n_seq * tiles * a.kv.n_kv * units);
+        *grid = (int)max(1ll, min((long long)*grid, a.b.n_seq * tiles * a.kv.n_kv * units));
     a.parts = carve_parts(a.parts.info, *grid, rows_of<MT>, false);
     kern<<<*grid, kThreads, smem, st>>>(a);
     return cudaGetLastError();

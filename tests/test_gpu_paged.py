@@ -690,6 +690,23 @@ def test_a_batch_with_no_rows_at_all(q2):
     assert (out == 7).all()
 
 
+def test_rows_against_a_bound_of_none(q2):
+    """max_q = 0: nothing to do if no sequence has a row, a guard code if one has."""
+    c = Case(q2, [(0, 5), (0, 9)], (8, 2, 64), "f16", 64, seed=43)
+    c.fill()
+    q = c.queries(torch.float16)
+    for starts, bad in (([0, 0, 0], False), ([0, 1, 2], True)):
+        b = q2.PagedBatch(torch.tensor(starts, dtype=torch.int32, device="cuda"), c.batch.kv_len, c.pages, 0)
+        out = torch.full_like(q, 7.0)
+        q2.paged_attention(c.kv, b, q, out=out)
+        if bad:
+            with pytest.raises(q2.Qwen2Error, match="q_start"):
+                b.check()
+        else:
+            b.check()
+        assert (out == 7).all()
+
+
 # ---- together, and with the model -------------------------------------------------------------
 
 
@@ -771,6 +788,23 @@ def test_model_sequences_are_parked_in_pages_and_resumed(q2, fmt):
                 m.save_pages(*bad, pools, pages)
         with pytest.raises(q2.Qwen2Error):
             m.save_pages(0, 40, pools[:1], pages)
+        m.synchronize()
+
+
+def test_parking_in_a_page_that_is_none_is_reported(q2):
+    """A page id outside the pools is left out, and check() of the returned batch says so; the rest is kept."""
+    shape = synth.SHAPES["toy"]
+    with q2.Qwen2Model(shape, synth.make_weights(shape, 0), n_ctx=64, max_seqs=2, max_tokens=64) as m:
+        m.prefill([0], [synth.make_tokens(shape.vocab, 40, 5)])
+        pools = [q2.PagedKV.zeros(4, 16, shape.n_kv_head, shape.head_dim, q2.KV_F16) for _ in range(shape.n_layer)]
+        pages = torch.tensor([2, 4, 3], dtype=torch.int32, device="cuda")
+        for call in (m.save_pages, m.load_pages):
+            with pytest.raises(q2.Qwen2Error, match="page id"):
+                call(0 if call == m.save_pages else 1, 40, pools, pages).check()
+        cache = m.kv_cache()
+        for rows in (slice(0, 16), slice(32, 40)):
+            assert torch.equal(cache[1, :, :, :, rows], cache[0, :, :, :, rows].half().float())
+        assert (cache[1, :, :, :, 16:32] == 0).all()
         m.synchronize()
 
 
