@@ -30,10 +30,10 @@
 // positions and warp (a third of them widens the codes), which fill 64% of the
 // issue slots with four CTAs an SM.  With the rows in M it took 88 us with
 // three CTAs an SM and 115 us with two (the registers of 64 accumulators more,
-// and a ring of four stages).  One token over 999 positions takes 7.6 us, of
+// and a ring of four stages).  One token over 999 positions takes 8 us, of
 // which the join and the two launches' latencies are some 4; the rest is a
 // chain of a few load latencies (lengths, page ids, pages) per CTA, and so it
-// is for 32 tokens over 256 - 4,095 of f16: 16.1 us for 36 MB.
+// is for 32 tokens over 256 - 4,095 of f16: 16.3 us for 36 MB.
 //
 // 8-bit pages: codes become exact f16 in registers (int8: 1024 + (c + 128)
 // by a byte permute, minus 1152; e4m3: the hardware conversion) and the f32

@@ -42,15 +42,15 @@
 // v's the probabilities, relative to G, the largest v scale so far rounded up
 // to a power of two, which O carries like the reference m.
 //
-// Measured: a prompt of 5,001 rows (28 heads on 4 of 128, bf16) 203 us, 883
-// TFLOP/s; 1,024 rows after 31,000 positions of e4m3 606 us, 763 TFLOP/s.  A
-// unit takes some 1,930 cycles, of which the products are about 1,950 for
-// both halves (16 of S at 79 cycles each, 8 of P V at 86): the tensor pipe is
-// what bounds it, at half its rate in S, since an M = 128 product of N = 64
-// takes as long as one of N = 128.  What is lost beside: 8,000 to 10,000
-// cycles where a CTA changes tiles (the last softmaxes, rows out through
-// shared memory, new queries), which is most of a short chunk's time, and the
-// join of cut tiles.
+// Measured: a prompt of 5,001 rows (28 heads on 4 of 128, bf16) 200 us, 895
+// TFLOP/s, the join's 15 us included; 1,024 rows after 31,000 positions of e4m3
+// 604 us, 766 TFLOP/s.  A unit takes some 1,930 cycles, as long as its products
+// take one after another (16 of S at 79 cycles each, 8 of P V at 86), S at half
+// the pipe's rate, since an M = 128 product of N = 64 takes as long as one of
+// N = 128 (the counters show the pipe busy 64% of the time).  Beside: 3,000 to
+// 8,000 cycles where a CTA changes tiles (the last softmaxes, rows out through
+// shared memory, new queries), and about 9,000 before its first product, which
+// with the join is most of a short chunk's time.
 //
 // V is the [position][dim] tile as it lies in the pages: an MN-major B
 // operand, so nothing is transposed.  Positions of the last unit that are no
