@@ -88,7 +88,7 @@ struct Meet {   // where the warps meet
     // g and g + 8 of an m tile side by side (MT = 0); the padding puts the rows
     // of one access into different banks.
     float o[rows_of<MT>][HD + (MT ? 16 : 4)];
-    float m[kWarps][rows_of<MT>], l[kWarps][rows_of<MT>], g[kWarps];
+    float m[kWarps][rows_of<MT>], l[kWarps][rows_of<MT>];
 };
 
 // 16-byte piece c of position r stands at piece c ^ f(r) of its row, so that
